@@ -320,7 +320,7 @@ def _plain_tables(s):
     fresh = change.clamp(min=0)
     tok_ptr = torch.cat([fresh.new_zeros(1), fresh.cumsum(0)])
     old, wide = (have + page - 1) // page, (want + page - 1) // page
-    fits = (wide <= max_pages) & (tok_ptr[1:] <= n_tok)
+    fits = (wide <= max_pages) & ((change <= 0) | (tok_ptr[1:] <= n_tok))
     need = torch.where(fits, (wide - old).clamp(min=0), 0)
     upto = need.cumsum(0)
     served = fits & ((need == 0) | (upto <= free))
