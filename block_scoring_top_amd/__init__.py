@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function here checks tensor placement and
 layout, passes raw device pointers and the current HIP stream to the C ABI
-(include/idx.h) and returns the output tensors. All arithmetic runs in the HIP
+(include/idx.h, include/idx_cache.h) and returns the output tensors. All arithmetic runs in the HIP
 kernels; there is no fallback path. PyTorch supplies device memory and streams.
 """
 from __future__ import annotations
@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -18,7 +19,9 @@ __all__ = ["idx_score", "idx_topk", "idx_topk_bf16", "idx_select", "idx_select_n
            "idx_topk_workspace_bytes", "idx_assign_workspace_bytes", "idx_status_string",
            "idx_floor_empty", "idx_floor_read", "idx_floor_mfma", "lib_path", "load", "IDX_SORTED", "IDX_RADIX8",
            "IdxError",
-           "SelectPlan", "plan_for"]
+           "SelectPlan", "plan_for",
+           "idx_page_tables", "PageTables", "idx_cache_write", "idx_attend", "idx_attend_prefill",
+           "idx_attend_workspace_bytes", "idx_attend_prefill_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libidx.so")
@@ -57,6 +60,18 @@ _SIGS = {
     "idx_plan_workspace_bytes": (_c_size, [_vp]),
     "idx_plan_select": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
     "idx_plan_destroy": (None, [_vp]),
+    "idx_page_tables": (_c_int, [_vp] * 13 + [_c_int, _c_int, _c_int, _c_int, ctypes.c_int64,
+                                              _c_int, _vp]),
+    "idx_cache_write": (_c_int, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp, _vp,
+                                 _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "idx_attend_workspace_bytes": (_c_size, [_c_int] * 6),
+    "idx_attend": (_c_int, [_vp, ctypes.c_int64] + [_vp] * 11 + [_c_int] * 6
+                   + [ctypes.c_int64, _c_int, _c_int, _c_int, ctypes.c_float, ctypes.c_float,
+                      _c_int, _vp, _c_size, _vp]),
+    "idx_attend_prefill_workspace_bytes": (_c_size, [_c_int] * 6),
+    "idx_attend_prefill": (_c_int, [_vp, ctypes.c_int64] + [_vp] * 10 + [_c_int] * 6
+                           + [ctypes.c_int64, _c_int, _c_int, ctypes.c_float, ctypes.c_float,
+                              _c_int, _vp, _c_size, _vp]),
     "idx_floor_empty": (_c_int, [_c_int, _vp]),
     "idx_floor_read": (_c_int, [_vp, _c_size, _vp, _vp, _c_int, _c_int, _vp]),
     "idx_floor_mfma": (_c_int, [_vp, _c_int, _c_int, _vp, _vp]),
@@ -371,6 +386,227 @@ def idx_assign(x, c, return_best=False, assign=None, best=None, ws=None):
     _check("idx_assign", lib.idx_assign(_ptr(x), _ptr(c), _ptr(assign), _ptr(best), N, C, D,
                                         _dtype_code(x), _ptr(ws), ws.numel(), _stream(dev)))
     return assign, best
+
+
+# ---- the paged 8-bit cache (include/idx_cache.h) --------------------------------------------
+
+class PageTables(NamedTuple):
+    """What idx_page_tables writes for the step (all int32)."""
+    seq_len: torch.Tensor      # [B] lengths after the step
+    cursor: torch.Tensor       # [3] head, free pages, requests refused
+    kv_indptr: torch.Tensor    # [B+1]
+    kv_indices: torch.Tensor   # [n_indices] the requests' pages, packed
+    tok_indptr: torch.Tensor   # [B+1] packed rows of the new tokens
+    slots: torch.Tensor        # [n_tokens] cache slot of each new token, -1: none
+    tok_req: torch.Tensor      # [n_tokens] its request, -1: none
+    tok_len: torch.Tensor      # [n_tokens] position + 1, 0: none
+
+
+def _int32(**ts):
+    for name, t in ts.items():
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+
+
+class _on:
+    """Makes a tensor's device the current one for the call (the kernels run on the
+    current device); nothing to do, and no cost, when it is already."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        index = torch.cuda.current_device()
+        self.back = None if self.dev.index == index else index
+        if self.back is not None:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def idx_page_tables(seq_len, n_new, table, free_ring, cursor, n_tokens, page_size=16,
+                    kv_indices=None):
+    """One step of the page allocator: request b holds seq_len[b] tokens in the pages
+    table[b] and changes by n_new[b] (negative: gives its last tokens back, -seq_len[b]
+    ends it). New pages come from free_ring at cursor = {head, count}; table and
+    free_ring are updated in place. Returns PageTables; seq_len and cursor of the next
+    step are its seq_len and cursor (n_tokens: rows of the packed new tokens;
+    kv_indices: a buffer for the packed pages, as long as free_ring by default)."""
+    lib = load()
+    dev = _dev(seq_len, n_new, table, free_ring, cursor, kv_indices)
+    _int32(seq_len=seq_len, n_new=n_new, table=table, free_ring=free_ring, cursor=cursor,
+           kv_indices=kv_indices)
+    B, max_pages = table.shape
+    n_pages = free_ring.numel()
+    if seq_len.numel() != B or n_new.numel() != B or cursor.numel() < 2:
+        raise ValueError("seq_len and n_new must hold an entry per table row, cursor two")
+    if n_tokens < 0:
+        raise ValueError("n_tokens must not be negative")
+    if kv_indices is None:
+        kv_indices = torch.empty(n_pages, dtype=torch.int32, device=dev)
+    # one allocation for the step's words, each list on a 16-byte border
+    up = lambda n: (n + 3) // 4 * 4  # noqa: E731
+    sizes = (B, 3, B + 1, B + 1, n_tokens, n_tokens, n_tokens)
+    buf = torch.empty(sum(up(n) for n in sizes), dtype=torch.int32, device=dev)
+    parts, at = [], 0
+    for n in sizes:
+        parts.append(buf[at:at + n])
+        at += up(n)
+    seq_out, cur_out, indptr, tok_indptr, slots, tok_req, tok_len = parts
+    with _on(dev):
+        _check("idx_page_tables", lib.idx_page_tables(
+            _ptr(seq_len), _ptr(n_new), _ptr(cursor), _ptr(table), _ptr(free_ring),
+            _ptr(seq_out), _ptr(cur_out), _ptr(indptr), _ptr(kv_indices), _ptr(tok_indptr),
+            _ptr(slots), _ptr(tok_req), _ptr(tok_len), B, max_pages, page_size, n_pages,
+            kv_indices.numel(), n_tokens, _stream(dev)))
+    return PageTables(seq_out, cur_out, indptr, kv_indices, tok_indptr, slots, tok_req, tok_len)
+
+
+def _rows(name, x, dev):
+    """A token-major tensor [n, heads, D] whose token rows may lie apart: its row
+    stride in elements."""
+    if not x.is_cuda or x.device != dev:
+        raise ValueError("all tensors must live on the same GPU")
+    if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise ValueError(f"{name} must be [tokens, heads, D] with dense heads")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale):
+    """Hkv, D, n_pages, page_size of a cache."""
+    for c in (k_cache, v_cache):
+        if c.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError("the caches must be float8_e4m3fn (or its codes as uint8)")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("the scales must be float32")
+    n_pages, Hkv, page, D = k_cache.shape
+    if tuple(v_cache.shape) != (n_pages, Hkv, D, page):
+        raise ValueError("v_cache must be [pages, Hkv, D, page_size] beside k_cache "
+                         "[pages, Hkv, page_size, D]")
+    if tuple(k_scale.shape) != (n_pages, Hkv) or tuple(v_scale.shape) != (n_pages, Hkv):
+        raise ValueError("the scales must be [pages, Hkv]")
+    return Hkv, D, n_pages, page
+
+
+def idx_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale):
+    """Quantises the keys and values k, v [n, Hkv, 128] (float32 or bf16; token rows may
+    lie apart) into their cache slots, one power-of-two scale per page and head. The
+    tokens of one page lie in consecutive rows (as idx_page_tables orders them)."""
+    lib = load()
+    dev = _dev(k_cache, v_cache, k_scale, v_scale, slots)
+    Hkv, D, n_pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _rows("k", k, dev), _rows("v", v, dev)
+    _int32(slots=slots)
+    n = slots.numel()
+    if tuple(k.shape) != (n, Hkv, D) or tuple(v.shape) != (n, Hkv, D) or k.dtype != v.dtype:
+        raise ValueError("k and v must be [slots, Hkv, D] of one dtype")
+    if k.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    with _on(dev):
+        _check("idx_cache_write", lib.idx_cache_write(
+            _ptr(k), _ptr(v), ks, vs, _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), n, Hkv, D, n_pages, page, _dtype_code(k), _stream(dev)))
+
+
+def idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K=0, page_size=16) -> int:
+    return load().idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K, page_size)
+
+
+def idx_attend_prefill_workspace_bytes(n_tok, B, Hq, Hkv, max_pages, page_size=16) -> int:
+    return load().idx_attend_prefill_workspace_bytes(n_tok, B, Hq, Hkv, max_pages, page_size)
+
+
+def _attend_inputs(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes,
+                   out, ws, scale, *more):
+    """Checks of both attention calls: (device, shapes, q's row stride, out, scale)."""
+    dev = _dev(k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes, out, ws,
+               *more)
+    shape = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    stride = _rows("q", q, dev)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    _int32(kv_indptr=kv_indptr, kv_indices=kv_indices, kv_len=kv_len)
+    n, Hq, D = q.shape
+    if D != shape[1]:
+        raise ValueError("q and the cache differ in head dimension")
+    if kv_len.numel() != n:
+        raise ValueError("kv_len must hold one entry per row of q")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != Hq):
+        raise ValueError("slopes must be float32, one per query head")
+    if out is None:
+        out = torch.empty(n, Hq, D, dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise ValueError("out must be bfloat16 and shaped as q")
+    return dev, shape, stride, out, (D ** -0.5 if scale is None else scale)
+
+
+def _scratch(nbytes, ws, dev):
+    """The workspace of an attention call: plain scratch, so it comes from torch's
+    allocator call by call (in stream order; inside a capture from the graph's own
+    memory) unless the caller brings one."""
+    if ws is not None or nbytes == 0:
+        return ws
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages,
+               row_req=None, ids=None, scale=None, softcap=0.0, slopes=None, out=None, ws=None):
+    """Attention of single tokens q [R, Hq, 128] (bf16) over the paged 8-bit cache: row r
+    sees the first kv_len[r] tokens of request row_req[r] (of request r without it), all
+    of them or, with ids [R, K], those of the selected page slots (-1: none), as
+    idx_select_paged returns them. softcap: scores become softcap * tanh(x / softcap);
+    slopes [Hq]: minus slope * distance. Returns out [R, Hq, 128]; a row that sees
+    nothing is zero."""
+    lib = load()
+    dev, (Hkv, D, n_pages, page), stride, out, scale = _attend_inputs(
+        q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes, out, ws,
+        scale, row_req, ids)
+    _int32(row_req=row_req, ids=ids)
+    R, Hq, _ = q.shape
+    B = kv_indptr.numel() - 1
+    if row_req is not None and row_req.numel() != R:
+        raise ValueError("row_req must hold one entry per row of q")
+    if ids is not None and (ids.dim() != 2 or ids.shape[0] != R):
+        raise ValueError("ids must be [rows, K]")
+    K = 0 if ids is None else ids.shape[1]
+    if ids is not None and K == 0:
+        return out.zero_()
+    ws = _scratch(lib.idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K, page), ws, dev)
+    with _on(dev):
+        _check("idx_attend", lib.idx_attend(
+            _ptr(q), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_len), _ptr(row_req), _ptr(ids),
+            _ptr(slopes), _ptr(out), R, B, Hq, Hkv, D, n_pages, kv_indices.numel(), max_pages,
+            page, K, scale, softcap, IDX_BF16, _ptr(ws), 0 if ws is None else ws.numel(),
+            _stream(dev)))
+    return out
+
+
+def idx_attend_prefill(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, tok_indptr,
+                       kv_len, max_pages, scale=None, softcap=0.0, slopes=None, out=None,
+                       ws=None):
+    """idx_attend for packed prompt tokens q [n, Hq, 128]: request b's rows are
+    tok_indptr[b]:tok_indptr[b+1], row t sees the first kv_len[t] tokens of its request
+    (PageTables.tok_len: the causal mask). Rows of no request keep their output."""
+    lib = load()
+    dev, (Hkv, D, n_pages, page), stride, out, scale = _attend_inputs(
+        q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes, out, ws,
+        scale, tok_indptr)
+    _int32(tok_indptr=tok_indptr)
+    n, Hq, _ = q.shape
+    B = kv_indptr.numel() - 1
+    if tok_indptr.numel() != B + 1:
+        raise ValueError("tok_indptr and kv_indptr must both hold B + 1 entries")
+    ws = _scratch(lib.idx_attend_prefill_workspace_bytes(n, B, Hq, Hkv, max_pages, page), ws, dev)
+    with _on(dev):
+        _check("idx_attend_prefill", lib.idx_attend_prefill(
+            _ptr(q), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(kv_indptr), _ptr(kv_indices), _ptr(tok_indptr), _ptr(kv_len), _ptr(slopes),
+            _ptr(out), n, B, Hq, Hkv, D, n_pages, kv_indices.numel(), max_pages, page, scale,
+            softcap, IDX_BF16, _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    return out
 
 
 def idx_floor_empty(blocks=1):

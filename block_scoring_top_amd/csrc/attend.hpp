@@ -1,0 +1,282 @@
+// Attention over the paged 8-bit cache: what its kernels share (gfx950, wave64).
+//
+// The online softmax runs in base 2 over tiles of 64 tokens. A tile is four units of
+// 16 tokens, each inside one page; lane group g = lane / 16 owns unit g. With keys as
+// the A operand of v_mfma_f32_16x16x32_bf16 and queries as B, row m of product s is
+// given token 4 s + m % 4 of unit m / 4, so that a lane's 16 scores (row 4 g + i of
+// s = 0..3) are the 16 tokens of its own unit for query row n = lane % 16:
+//   - the unit's page scales are one number per lane;
+//   - the probabilities of eight consecutive tokens are already in the lane that needs
+//     them as the B operand of the second product, whose A operand, the values of
+//     those tokens at one dim, is 8 consecutive bytes of the value cache;
+// so neither scores nor values cross lanes, and both caches go straight from memory
+// into registers, 16 bytes a lane.
+// A probability is held as 2^(x - m + kPBias): fp16 then keeps 11 bits of every
+// probability down to 2^-28 of the row's largest.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace idxk {
+
+typedef __bf16 at_bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 at_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 at_f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 at_f16x2 __attribute__((ext_vector_type(2)));
+typedef float at_f32x2 __attribute__((ext_vector_type(2)));
+typedef float at_f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kUnit = 16;       // tokens of a unit
+constexpr int kTileTok = 64;    // tokens of a tile: one unit per lane group
+constexpr float kPBias = 14.f;  // probabilities reach 2^14
+constexpr float kLog2e = 1.4426950408889634f;
+
+// four e4m3 codes -> bf16 / fp16 (both exact)
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&o)[2]) {
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true));
+}
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[2]) {
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true));
+}
+__device__ __forceinline__ at_bf16x8 codes_bf16x8(uint32_t lo, uint32_t hi) {
+  uint32_t a[2], b[2];
+  codes_bf16(lo, a);
+  codes_bf16(hi, b);
+  return __builtin_bit_cast(at_bf16x8, make_uint4(a[0], a[1], b[0], b[1]));
+}
+__device__ __forceinline__ at_f16x8 codes_f16x8(uint32_t lo, uint32_t hi) {
+  uint32_t a[2], b[2];
+  codes_f16(lo, a);
+  codes_f16(hi, b);
+  return __builtin_bit_cast(at_f16x8, make_uint4(a[0], a[1], b[0], b[1]));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  at_f32x2 f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, at_f16x2));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  at_f32x2 f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, at_bf16x2));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// over the four lane groups of one query row
+__device__ __forceinline__ float groups_max(float v) {
+  v = fmaxf(v, __uint_as_float(lane_xor<16>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(lane_xor<32>(__float_as_uint(v))));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+  v += __uint_as_float(lane_xor<16>(__float_as_uint(v)));
+  return v + __uint_as_float(lane_xor<32>(__float_as_uint(v)));
+}
+
+// The score of one token in base-2 units. ksc holds the page's key scale, the call's
+// scale and, for uncapped scores, log2(e); dist = visible length - 1 - position.
+template <bool EXTRA>
+__device__ __forceinline__ float score2(float dot, float ksc, float softcap, float slope2,
+                                        float dist) {
+  float x = dot * ksc;
+  if constexpr (EXTRA) {
+    if (softcap > 0.f) {
+      // tanh y = 1 - 2 / (1 + e^(2y)): y large gives 1, y small -1, no overflow
+      const float e = exp2_fast(x * (2.f * kLog2e / softcap));
+      x = softcap * kLog2e * (1.f - 2.f / (1.f + e));
+    }
+    x -= slope2 * dist;
+  }
+  return x;
+}
+
+// the running softmax of NT tiles of 16 query rows
+template <int NT>
+struct AttnState {
+  at_f32x4 o[NT][8];  // dims 16 dt + 4 g + i of query row n
+  float m[NT], l[NT];  // m: all groups alike; l: this group's units alone
+  float vref;          // largest value scale met: o is in its units
+};
+
+template <int NT>
+__device__ __forceinline__ void attn_init(AttnState<NT>& st) {
+  st.vref = 0.f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    st.m[j] = -__builtin_inff();
+    st.l[j] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt) st.o[j][dt] = at_f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// Query rows of a lane as the B operand: chunk (c, half) holds dims
+// 64 c + 16 g + 8 half .. + 7 of query row n.
+__device__ __forceinline__ void load_query(const uint16_t* row, int g, at_bf16x8 (&q)[4]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      q[2 * c + half] = __builtin_bit_cast(
+          at_bf16x8, *reinterpret_cast<const uint4*>(row + 64 * c + 16 * g + 8 * half));
+}
+
+// One tile. k: this lane's key bytes, k[s][c] = dims 64 c + 16 g .. + 15 of token
+// 4 s + m % 4 of unit m / 4; v[dt]: the 16 tokens of unit g at dim 16 dt + n.
+// ksc: the score scale of unit g; vs: its value scale, 0 if it holds no token; pos:
+// position of its first token; have: how many of its tokens exist; len: visible length
+// of each of the lane's query rows; any: whether a token of the tile is masked for any
+// row (uniform over the wave).
+template <int NT, bool EXTRA>
+__device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q)[NT][4],
+                                          const uint4 (&k)[4][2], const uint4 (&v)[8], float ksc,
+                                          float vs, int pos, int have, const int (&len)[NT],
+                                          const float (&slope2)[NT], float softcap, bool any) {
+  // Values enter the product as bare codes; their scales go into the probabilities,
+  // relative to the largest one met, so that fp16 holds them.
+  const float vtop = groups_max(vs);
+  if (vtop > st.vref) {
+    const float f = st.vref / vtop;
+    st.vref = vtop;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt) st.o[j][dt] *= f;
+  }
+  const float vsc = vs == st.vref ? 1.f : vs / st.vref;
+  at_f32x4 x[NT][4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x[j][s] = at_f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const at_bf16x8 k0 = codes_bf16x8(k[s][c].x, k[s][c].y);
+      const at_bf16x8 k1 = codes_bf16x8(k[s][c].z, k[s][c].w);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        x[j][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[j][2 * c], x[j][s], 0, 0, 0);
+        x[j][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[j][2 * c + 1], x[j][s], 0, 0, 0);
+      }
+    }
+  }
+  uint4 p[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 4 * s + i;
+        float y = score2<EXTRA>(x[j][s][i], ksc, softcap, slope2[j],
+                                EXTRA ? (float)(len[j] - 1 - pos - tok) : 0.f);
+        if (any) y = (tok < have && pos + tok < len[j]) ? y : -__builtin_inff();
+        x[j][s][i] = y;
+        top = fmaxf(top, y);
+      }
+    const float m = fmaxf(st.m[j], groups_max(top));
+    const float base = (m == -__builtin_inff() ? 0.f : m);
+    const float alpha = exp2_fast(st.m[j] - base);
+    st.m[j] = m;
+    float sum = 0.f;
+    uint32_t w[8];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      float e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[i] = exp2_fast(x[j][s][i] - (base - kPBias));
+        sum += e[i];
+        e[i] *= vsc;
+      }
+      w[2 * s] = pack_f16(e[0], e[1]);
+      w[2 * s + 1] = pack_f16(e[2], e[3]);
+    }
+    p[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
+    p[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
+    st.l[j] = st.l[j] * alpha + sum;
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt) st.o[j][dt] *= alpha;
+  }
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt) {
+    const at_f16x8 v0 = codes_f16x8(v[dt].x, v[dt].y);
+    const at_f16x8 v1 = codes_f16x8(v[dt].z, v[dt].w);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      st.o[j][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          v0, __builtin_bit_cast(at_f16x8, p[j][0]), st.o[j][dt], 0, 0, 0);
+      st.o[j][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          v1, __builtin_bit_cast(at_f16x8, p[j][1]), st.o[j][dt], 0, 0, 0);
+    }
+  }
+}
+
+// zeroes the codes of the tokens from `have` on (whatever they hold, NaN included,
+// they would meet a probability of zero)
+__device__ __forceinline__ uint4 keep_tokens(uint4 v, int have) {
+  auto word = [&](uint32_t w, int first) -> uint32_t {
+    const int n = have - first;
+    return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
+  };
+  return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
+}
+
+// Whether a code is NaN: low seven bits all set.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// In a tile that some rows see only in part, a NaN value code must reach the rows that
+// see its token and no others, though all rows share the product (0 x NaN = NaN).
+// Replaces NaN codes by zero and puts NaN into the sums of the rows that see them: the
+// product of "code is NaN" with "row sees token" is positive exactly there.
+template <int NT>
+__device__ __forceinline__ void attn_nan_values(AttnState<NT>& st, uint4 (&v)[8], int pos,
+                                                int have, const int (&len)[NT]) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt)
+    bad |= nan_codes(v[dt].x) | nan_codes(v[dt].y) | nan_codes(v[dt].z) | nan_codes(v[dt].w);
+  if (!__any(bad != 0)) return;
+  uint4 sees[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    uint32_t w[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      auto one = [&](int tok) { return tok < have && pos + tok < len[j] ? 0x3C00u : 0u; };
+      w[t] = one(2 * t) | (one(2 * t + 1) << 16);
+    }
+    sees[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
+    sees[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt) {
+    uint32_t w[4] = {v[dt].x, v[dt].y, v[dt].z, v[dt].w}, is[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t n = nan_codes(w[e]) >> 7;  // 1 in each NaN byte
+      is[e] = n * 0x38u;                        // e4m3 1.0 there
+      w[e] &= ~(n * 0xFFu);
+    }
+    v[dt] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      at_f32x4 hit = {0.f, 0.f, 0.f, 0.f};
+      hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          codes_f16x8(is[0], is[1]), __builtin_bit_cast(at_f16x8, sees[j][0]), hit, 0, 0, 0);
+      hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          codes_f16x8(is[2], is[3]), __builtin_bit_cast(at_f16x8, sees[j][1]), hit, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (hit[i] > 0.f) st.o[j][dt][i] = __builtin_nanf("");
+    }
+  }
+}
+
+}  // namespace idxk

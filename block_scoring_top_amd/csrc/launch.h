@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "attend_args.h"
+
 namespace idxk {
 
 int launch_score(const void* q, const void* c, const int32_t* seq_len, float* scores, int B,
@@ -70,5 +72,26 @@ int launch_pool_keys(const void* k, const int32_t* seq_len, void* c, int B, int 
 int launch_prefill_score(const void* q, const void* c, const int32_t* pos0, float* scores,
                          int64_t row_stride, int32_t* n_valid, int B, int T, int H, int N_pad,
                          int page_size, bool fill_dead, void* stream);
+
+// One step of the page allocator (idx_page_tables).
+int launch_page_tables(const int32_t* seq_len, const int32_t* n_new, const int32_t* cursor,
+                       int32_t* table, int32_t* ring, int32_t* seq_out, int32_t* cursor_out,
+                       int32_t* kv_indptr, int32_t* kv_indices, int32_t* tok_indptr,
+                       int32_t* slots, int32_t* tok_req, int32_t* tok_len, int B, int max_pages,
+                       int page_size, int n_pages, int64_t n_indices, int n_tok, void* stream);
+
+// Quantising write of new keys and values (idx_cache_write).
+int launch_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                       const int32_t* slots, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+                       float* v_scale, int n_tok, int Hkv, int n_pages, int page_size, bool bf16,
+                       void* stream);
+
+// How a call's rows of `units` 16-token units are cut (host only), and the calls
+// (idx_attend, idx_attend_prefill); splits > 1 needs part_o and part_ml.
+AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units);
+AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units);
+int64_t attend_prefill_tiles(int64_t n_tok, int B, int G);  // workgroups per head and split
+int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream);
+int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
 
 }  // namespace idxk
