@@ -23,7 +23,7 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", os.path.join(ROOT, "include")]
 
 HIP_SOURCES = ["indexer.hip", "indexer_radix8.hip", "assign.hip", "prefill.hip", "pool.hip",
-               "floor.hip", "tables.hip", "cache_write.hip", "attend.hip"]
+               "floor.hip", "tables.hip", "cache_write.hip", "attend.hip", "attend_prefill.hip"]
 # assign.hip's inputs are finite by contract; without NaN semantics its running
 # max compiles to plain 3-input maxes (no per-operand canonicalisation)
 EXTRA_FLAGS = {"assign.hip": ["-fno-honor-nans"]}

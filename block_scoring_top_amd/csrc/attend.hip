@@ -1,14 +1,11 @@
-// Attention over the paged 8-bit cache (include/idx_cache.h: idx_attend,
-// idx_attend_prefill). The tile that both kernels run is in attend.hpp.
+// Attention of single tokens over the paged 8-bit cache (include/idx_cache.h,
+// idx_attend), and the join of partial results. The tile is in attend.hpp.
 //
-// attend_rows_kernel: one token's query heads of one KV head are the 16 (32, 64)
-// rows of the products. Bound by reading the cache, 256 bytes a token and KV head:
-// each of a workgroup's four waves runs its own tiles, with its own softmax, joined
-// in LDS at the end. Long rows are cut into chunks of tiles for several workgroups;
-// their partial sums are joined by attend_merge_kernel.
-//
-// attend_prefill_kernel: 128 rows (token, head of the group) of one request share
-// the tiles, 32 rows to a wave.
+// One token's query heads of one KV head are the 16 (32, 64) rows of the products.
+// Bound by reading the cache, 256 bytes a token and KV head: each of a workgroup's four
+// waves runs its own tiles, with its own softmax, joined in LDS at the end. Long rows are
+// cut into chunks of tiles for several workgroups; their partial sums are joined by
+// attend_merge_kernel.
 #include <hip/hip_runtime.h>
 
 #include "attend.hpp"
@@ -24,26 +21,6 @@ constexpr int kAtWaves = kAtNT / kWave;
 constexpr int kChunkTiles = 256;              // most tiles of one workgroup
 constexpr int kChunkUnits = 4 * kChunkTiles;
 constexpr int kRowPad = kHeadDim + 4;         // floats of a row of sums in LDS
-
-// The page list of a request.
-struct PageList {
-  int64_t base;
-  int n;  // pages
-};
-__device__ __forceinline__ PageList page_list(const AttnArgs& a, int b) {
-  const int64_t lo = a.kv_indptr[b], hi = a.kv_indptr[b + 1];
-  const int64_t n = hi - lo;
-  return {lo, (int)(n < 0 ? 0 : n < a.max_pages ? n : a.max_pages)};
-}
-// The cache block (page, head) of a list slot, or -1.
-__device__ __forceinline__ int block_of(const AttnArgs& a, const PageList& p, int slot, int h) {
-  if (slot < 0 || slot >= p.n) return -1;
-  const int64_t at = p.base + slot;
-  if (at < 0 || at >= a.n_indices) return -1;
-  const int page = a.kv_indices[at];
-  if (page < 0 || page >= a.n_pages) return -1;
-  return page * a.Hkv + h;
-}
 
 // Loads of one tile: this lane's key bytes (unit m / 4) and value bytes (unit g).
 __device__ __forceinline__ void load_tile(const AttnArgs& a, int kblk, int ksub, int vblk,
@@ -62,10 +39,6 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, int kblk, int ksub,
 #pragma unroll
   for (int dt = 0; dt < 8; ++dt)
     v[dt] = *reinterpret_cast<const uint4*>(vp + (int64_t)dt * 16 * a.page_size);
-}
-
-__device__ __forceinline__ float slope_of(const AttnArgs& a, int hq) {
-  return a.slopes == nullptr ? 0.f : a.slopes[hq] * kLog2e;
 }
 
 template <int NT, bool EXTRA>
@@ -236,123 +209,6 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
       pack_bf16(o[0] * inv, o[1] * inv);
 }
 
-constexpr int kPreRows = 128;  // rows of a workgroup, 32 to a wave
-
-// First tile of request b in the grid: tiles never span requests, and
-// floor(y / T) - floor(x / T) + 1 tiles hold any x..y rows.
-__device__ __forceinline__ int64_t first_tile(const AttnArgs& a, int b, int G) {
-  const int64_t p = min(max(a.tok_indptr[b], 0), a.R);
-  return p * G / kPreRows + b;
-}
-
-template <bool EXTRA>
-__global__ __launch_bounds__(kAtNT) void attend_prefill_kernel(AttnArgs a, int chunk,
-                                                               int splits) {
-  constexpr int NT = 2;
-  const int h = blockIdx.x % a.Hkv;
-  const int rest = blockIdx.x / a.Hkv;
-  const int split = rest % splits;
-  const int64_t tile = rest / splits;
-  const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
-  const int n = lane & 15, g = lane >> 4;
-  const int G = a.Hq / a.Hkv;
-  const int upp = a.page_size / kUnit;
-
-  // the tile's request: the last b with first_tile(b) <= tile
-  int b = 0;
-  for (int lo = 0, hi = a.B; lo < hi;) {
-    const int mid = (lo + hi) / 2;
-    if (first_tile(a, mid, G) <= tile) {
-      b = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid;
-    }
-  }
-  const int t0 = min(max(a.tok_indptr[b], 0), a.R);
-  const int t1 = min(max(a.tok_indptr[b + 1], 0), a.R);
-  const int64_t row0 = (tile - first_tile(a, b, G)) * kPreRows;
-  const int64_t rows = (int64_t)(t1 - t0) * G;
-  if (row0 < 0 || row0 >= rows) return;
-
-  const PageList pages = page_list(a, b);
-  at_bf16x8 q[NT][4];
-  float slope2[NT];
-  int len[NT];
-  int64_t where[NT];  // output row, -1: none
-  int longest = 0, shortest = 0x7FFFFFFF;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t row = row0 + 32 * w + 16 * j + n;
-    const int64_t at = min(row, rows - 1);
-    const int64_t tok = t0 + at / G;
-    const int hq = h * G + (int)(at % G);
-    load_query(a.q + tok * a.q_stride + hq * kHeadDim, g, q[j]);
-    slope2[j] = EXTRA ? slope_of(a, hq) : 0.f;
-    len[j] = max(a.kv_len[tok], 0);
-    where[j] = row < rows ? tok * a.Hq + hq : -1;
-    longest = max(longest, len[j]);
-    shortest = min(shortest, len[j]);
-  }
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) {
-    longest = max(longest, __shfl_xor(longest, d));
-    shortest = min(shortest, __shfl_xor(shortest, d));
-  }
-  AttnState<NT> st;
-  attn_init(st);
-
-  const int64_t units = min((int64_t)pages.n * upp, ((int64_t)longest + kUnit - 1) / kUnit);
-  const int64_t tiles = (units + 3) / 4;
-  const int64_t end = min(tiles, (int64_t)(split + 1) * chunk);
-  for (int64_t t = (int64_t)split * chunk; t < end; ++t) {
-    const int64_t ku = 4 * t + (n >> 2), vu = 4 * t + g;
-    const int kblk = ku < units ? block_of(a, pages, (int)(ku / upp), h) : -1;
-    const int vblk = vu < units ? block_of(a, pages, (int)(vu / upp), h) : -1;
-    const int pos = vblk < 0 ? 0 : (int)vu * kUnit;
-    const int have = vblk < 0 ? 0 : min(longest - pos, kUnit);
-    const float ks = vblk < 0 ? 0.f : a.k_scale[vblk] * a.score_scale;
-    const float vs = vblk < 0 ? 0.f : a.v_scale[vblk];
-    uint4 k[4][2], v[8];
-    load_tile(a, kblk, (int)(ku % upp), vblk, (int)(vu % upp), n, g, k, v);
-    const bool any = !__all(have == kUnit && pos + kUnit <= shortest);
-    if (any) {
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
-      attn_nan_values<NT>(st, v, pos, have, len);
-    }
-    attn_tile<NT, EXTRA>(st, q, k, v, ks, vs, pos, have, len, slope2, a.softcap, any);
-  }
-
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const float l = groups_sum(st.l[j]);
-    if (where[j] < 0) continue;
-    if (splits == 1) {
-      const float inv = l == 0.f ? 0.f : st.vref / l;
-      uint16_t* o = a.out + where[j] * kHeadDim;
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt) {
-        const at_f32x4 x = st.o[j][dt];
-        *reinterpret_cast<uint2*>(o + 16 * dt + 4 * g) =
-            make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-      }
-    } else {
-      const int64_t tok = where[j] / a.Hq;
-      const int row = (int)(where[j] % a.Hq) % G;
-      const int64_t part = (((tok * a.Hkv + h) * splits) + split) * G + row;
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt)
-        *reinterpret_cast<at_f32x4*>(a.part_o + part * kHeadDim + 16 * dt + 4 * g) =
-            st.o[j][dt] * st.vref;
-      if (g == 0) {
-        a.part_ml[2 * part] = st.m[j];
-        a.part_ml[2 * part + 1] = l;
-      }
-    }
-  }
-}
-
 }  // namespace
 
 AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
@@ -366,22 +222,11 @@ AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
   return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
 }
 
-AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
-  const int64_t tiles = (units + 3) / 4;
-  const int64_t groups = attend_prefill_tiles(n_tok, B, Hq / Hkv) * Hkv;
-  int64_t splits = (512 + groups - 1) / groups;
-  splits = splits < tiles / 8 ? splits : tiles / 8;
-  if (splits < 1) splits = 1;
-  const int64_t chunk = (tiles + splits - 1) / splits;
-  return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
-}
-
-int64_t attend_prefill_tiles(int64_t n_tok, int B, int G) { return n_tok * G / kPreRows + B; }
-
-static int launch_merge(const AttnArgs& a, int64_t rows, int splits, hipStream_t s) {
+int launch_attend_merge(const AttnArgs& a, int splits, void* stream) {
+  const int64_t rows = a.R;
   const int64_t grid = (rows * a.Hq + kAtWaves - 1) / kAtWaves;
-  hipLaunchKernelGGL(attend_merge_kernel, dim3((unsigned)grid), dim3(kAtNT), 0, s, a, rows,
-                     splits);
+  hipLaunchKernelGGL(attend_merge_kernel, dim3((unsigned)grid), dim3(kAtNT), 0,
+                     static_cast<hipStream_t>(stream), a, rows, splits);
   return (int)hipGetLastError();
 }
 
@@ -401,21 +246,7 @@ int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream) {
   }
 #undef IDX_ROWS
   int e = (int)hipGetLastError();
-  if (e == 0 && sp.splits > 1) e = launch_merge(a, a.R, sp.splits, s);
-  return e;
-}
-
-int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool extra = a.softcap > 0.f || a.slopes != nullptr;
-  const int64_t tiles = attend_prefill_tiles(a.R, a.B, a.Hq / a.Hkv);
-  const dim3 grid((unsigned)(tiles * a.Hkv * sp.splits)), blk(kAtNT);
-#define IDX_PRE(EX) \
-  hipLaunchKernelGGL((attend_prefill_kernel<EX>), grid, blk, 0, s, a, sp.chunk, sp.splits)
-  if (extra) IDX_PRE(true); else IDX_PRE(false);
-#undef IDX_PRE
-  int e = (int)hipGetLastError();
-  if (e == 0 && sp.splits > 1) e = launch_merge(a, a.R, sp.splits, s);
+  if (e == 0 && sp.splits > 1) e = launch_attend_merge(a, sp.splits, stream);
   return e;
 }
 

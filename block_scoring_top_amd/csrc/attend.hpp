@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attend_args.h"
 #include "common.hpp"
 
 namespace idxk {
@@ -231,52 +232,28 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// In a tile that some rows see only in part, a NaN value code must reach the rows that
-// see its token and no others, though all rows share the product (0 x NaN = NaN).
-// Replaces NaN codes by zero and puts NaN into the sums of the rows that see them: the
-// product of "code is NaN" with "row sees token" is positive exactly there.
-template <int NT>
-__device__ __forceinline__ void attn_nan_values(AttnState<NT>& st, uint4 (&v)[8], int pos,
-                                                int have, const int (&len)[NT]) {
-  uint32_t bad = 0;
-#pragma unroll
-  for (int dt = 0; dt < 8; ++dt)
-    bad |= nan_codes(v[dt].x) | nan_codes(v[dt].y) | nan_codes(v[dt].z) | nan_codes(v[dt].w);
-  if (!__any(bad != 0)) return;
-  uint4 sees[NT][2];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    uint32_t w[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      auto one = [&](int tok) { return tok < have && pos + tok < len[j] ? 0x3C00u : 0u; };
-      w[t] = one(2 * t) | (one(2 * t + 1) << 16);
-    }
-    sees[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
-    sees[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-#pragma unroll
-  for (int dt = 0; dt < 8; ++dt) {
-    uint32_t w[4] = {v[dt].x, v[dt].y, v[dt].z, v[dt].w}, is[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t n = nan_codes(w[e]) >> 7;  // 1 in each NaN byte
-      is[e] = n * 0x38u;                        // e4m3 1.0 there
-      w[e] &= ~(n * 0xFFu);
-    }
-    v[dt] = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      at_f32x4 hit = {0.f, 0.f, 0.f, 0.f};
-      hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-          codes_f16x8(is[0], is[1]), __builtin_bit_cast(at_f16x8, sees[j][0]), hit, 0, 0, 0);
-      hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-          codes_f16x8(is[2], is[3]), __builtin_bit_cast(at_f16x8, sees[j][1]), hit, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (hit[i] > 0.f) st.o[j][dt][i] = __builtin_nanf("");
-    }
-  }
+// The page list of a request.
+struct PageList {
+  int64_t base;
+  int n;  // pages
+};
+__device__ __forceinline__ PageList page_list(const AttnArgs& a, int b) {
+  const int64_t lo = a.kv_indptr[b], hi = a.kv_indptr[b + 1];
+  const int64_t n = hi - lo;
+  return {lo, (int)(n < 0 ? 0 : n < a.max_pages ? n : a.max_pages)};
+}
+// The cache block (page, head) of a list slot, or -1.
+__device__ __forceinline__ int block_of(const AttnArgs& a, const PageList& p, int slot, int h) {
+  if (slot < 0 || slot >= p.n) return -1;
+  const int64_t at = p.base + slot;
+  if (at < 0 || at >= a.n_indices) return -1;
+  const int page = a.kv_indices[at];
+  if (page < 0 || page >= a.n_pages) return -1;
+  return page * a.Hkv + h;
+}
+
+__device__ __forceinline__ float slope_of(const AttnArgs& a, int hq) {
+  return a.slopes == nullptr ? 0.f : a.slopes[hq] * kLog2e;
 }
 
 }  // namespace idxk

@@ -93,5 +93,6 @@ AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t un
 int64_t attend_prefill_tiles(int64_t n_tok, int B, int G);  // workgroups per head and split
 int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
+int launch_attend_merge(const AttnArgs& a, int splits, void* stream);
 
 }  // namespace idxk

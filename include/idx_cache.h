@@ -135,7 +135,7 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * Scores, softmax statistics and sums are fp32; keys and queries meet as exact
  * bf16 products; a probability is rounded to 11 bits (fp16) before it meets its
  * value, whose e4m3 code is exact there. That holds while the value scales of
- * one head that matter lie within 2^28 of each other.
+ * one head that matter lie within 2^20 of each other.
  * scale finite; softcap finite, >= 0 (0: none). R >= 0 (0: nothing is enqueued),
  * 1 <= Hq / Hkv <= IDX_MAX_GROUP, Hq a multiple of Hkv, page_size 16, 32 or 64.
  * ws: at least idx_attend_workspace_bytes(...) bytes (256-byte aligned; may be

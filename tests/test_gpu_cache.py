@@ -521,6 +521,33 @@ def test_prefill_bad_pages():
 
 # ------------------------------------------------------------------- together
 
+@pytest.mark.parametrize("scale,cap", [(-0.2, 0.0), (-0.2, 4.0), (0.0, 0.0), (3.0, 0.0)])
+def test_call_scales_of_any_sign_and_size(scale, cap):
+    lens, news = [300, 77], [40, 77]
+    c = Cache(49, lens, 2, 16)
+    ptr, req, seen = causal(lens, news)
+    q, q64 = queries(c.rng, len(req), 6)
+    kw = dict(scale=scale, softcap=cap)
+    check_rows(prefill(c, q, ptr, seen, **kw), c, q64, req, seen, scale=scale, cap=cap)
+    check_rows(attend(c, q, seen, row_req=i32(req), **kw), c, q64, req, seen, scale=scale,
+               cap=cap)
+
+
+def test_value_scales_that_grow_along_the_row():
+    """Each page's value scale above the ones before it, the last tiles' by far."""
+    lens = [6000]
+    c = Cache(51, lens, 1, 16)
+    n = len(c.indices)
+    c.vs[c.indices, 0] = np.exp2(np.linspace(-14, 0, n)).astype(np.float32)
+    c.ks[c.indices, 0] = np.exp2(np.linspace(-9, -5, n)).astype(np.float32)
+    c.k[c.indices[7]], c.v[c.indices[7]] = 0, 0           # a page of zeros: the least scale
+    c.ks[c.indices[7]] = c.vs[c.indices[7]] = 2.0 ** -120
+    ptr, req, seen = causal(lens, [40])
+    q, q64 = queries(c.rng, 40, 4)
+    check_rows(prefill(c, q, ptr, seen), c, q64, req, seen)
+    check_rows(attend(c, q, seen, row_req=i32(req)), c, q64, req, seen)
+
+
 def test_rows_and_prompt_tokens_agree():
     """The same rows through both calls: equal within both bounds of the oracle."""
     lens, news = [700, 90, 1300], [5, 1, 3]
