@@ -77,6 +77,13 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v + __uint_as_float(lane_xor<32>(__float_as_uint(v)));
 }
 
+// cap * tanh(x / cap) in base-2 units, by tanh y = 1 - 2 / (1 + e^(2y)): y large gives
+// 1, y small -1, no overflow
+__device__ __forceinline__ float capped(float x, float cap) {
+  const float e = exp2_fast(x * (2.f * kLog2e / cap));
+  return cap * kLog2e * __builtin_fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + e), 1.f);
+}
+
 // The score of one token in base-2 units. ksc holds the page's key scale, the call's
 // scale and, for uncapped scores, log2(e); dist = visible length - 1 - position.
 template <bool EXTRA>
@@ -84,11 +91,7 @@ __device__ __forceinline__ float score2(float dot, float ksc, float softcap, flo
                                         float dist) {
   float x = dot * ksc;
   if constexpr (EXTRA) {
-    if (softcap > 0.f) {
-      // tanh y = 1 - 2 / (1 + e^(2y)): y large gives 1, y small -1, no overflow
-      const float e = exp2_fast(x * (2.f * kLog2e / softcap));
-      x = softcap * kLog2e * (1.f - 2.f / (1.f + e));
-    }
+    if (softcap > 0.f) x = capped(x, softcap);
     x -= slope2 * dist;
   }
   return x;

@@ -38,6 +38,8 @@ constexpr int kPhaseTiles = 64;               // tiles whose page data wait in L
 constexpr int kPhaseUnits = 4 * kPhaseTiles;
 constexpr float kPreBias = 9.f;
 constexpr float kLazy = 6.f;
+// what happens to a score beside its scale; capped ones may be biased too
+constexpr int kPlain = 0, kBiased = 1, kCapped = 2;
 constexpr int kFrag = kWave;                  // uint4s of one operand in LDS
 
 struct PreLds {
@@ -46,8 +48,11 @@ struct PreLds {
   int u_blk[kPhaseUnits];
   float u_ks[kPhaseUnits], u_lv[kPhaseUnits];
   float red[kPreWaves];
-  int longest[kPreWaves];
+  int longest[kPreWaves], shortest[kPreWaves];
+  // NaN value codes of a tile that some rows see only in part: which tile (plus one),
+  // and for each dim and unit which of its 16 tokens
   int nan_tile[2];
+  uint16_t nan_map[2][kHeadDim][4];
 };
 
 // First workgroup of request b: tiles never span requests, and
@@ -61,7 +66,7 @@ __device__ __forceinline__ float halves_max(float v) {
   return fmaxf(v, __uint_as_float(lane_xor<32>(__float_as_uint(v))));
 }
 
-template <bool EXTRA>
+template <int KIND>
 __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int chunk,
                                                                 int splits, int64_t n_tiles) {
   __shared__ PreLds lds;
@@ -72,7 +77,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
   const int n = lane & 31, half = lane >> 5;
   const int G = a.Hq / a.Hkv;
-  const int upp = a.page_size / kUnit;
+  const int ush = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(units a page)
 
   // the tile's request: the last b with first_tile(b) <= tile
   int b = 0;
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   const int64_t tok = t0 + rat / G;
   const int hq = h * G + (int)(rat % G);
   const int len = max(a.kv_len[tok], 0);
-  const float slope2 = EXTRA ? slope_of(a, hq) : 0.f;
+  const float slope2 = KIND != kPlain ? slope_of(a, hq) : 0.f;
   // dims 16 s + 8 half .. + 7 of the row; a negative call scale turns the queries'
   // signs, so that scores keep their order under the (positive) scale of a unit
   at_bf16x8 q[8];
@@ -119,11 +124,18 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     longest = max(longest, __shfl_xor(longest, d));
     shortest = min(shortest, __shfl_xor(shortest, d));
   }
-  if (lane == 0) lds.longest[w] = longest;
+  if (lane == 0) {
+    lds.longest[w] = longest;
+    lds.shortest[w] = shortest;
+  }
+  if (tid < 2) lds.nan_tile[tid] = 0;
   __syncthreads();
-  int most = 0;
+  int most = 0, least = 0x7FFFFFFF;  // of the workgroup's rows
 #pragma unroll
-  for (int i = 0; i < kPreWaves; ++i) most = max(most, lds.longest[i]);
+  for (int i = 0; i < kPreWaves; ++i) {
+    most = max(most, lds.longest[i]);
+    least = min(least, lds.shortest[i]);
+  }
 
   at_f32x16 o[4];
 #pragma unroll
@@ -132,32 +144,31 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m = -__builtin_inff(), l = 0.f, vref = 0.f;
 
-  const int64_t units = min((int64_t)pages.n * upp, ((int64_t)most + kUnit - 1) / kUnit);
-  const int64_t tiles = (units + 3) / 4;
-  const int64_t begin = (int64_t)split * chunk;
-  const int64_t end = min(tiles, begin + chunk);
+  const int units = min(pages.n << ush, (int)(((int64_t)most + kUnit - 1) / kUnit));
+  const int begin = split * chunk;
+  const int end = min((units + 3) / 4, begin + chunk);
 
   // staging: thread -> (token, 16 dims) of the keys and (unit, dim) of the values
   const int64_t block = (int64_t)a.page_size * kHeadDim;
+  const int sub = (1 << ush) - 1;
   const int ktok = (tid & 7) | ((tid >> 6) << 3), kc = (tid >> 3) & 7;  // 8 tokens a wave
   const int ku = ktok >> 4;
   const int vd = tid & 127, vu = tid >> 7;
   uint4 kreg, vreg;
   int vhave = 0;  // visible tokens of this thread's value unit
   bool kval = false;
-  auto load = [&](int64_t t, int64_t phase) {
-    const int i = (int)(t - phase) * 4;
+  auto load = [&](int t, int phase) {
+    const int i = (t - phase) * 4;
     const int kb = lds.u_blk[i + ku], vb = lds.u_blk[i + vu];
-    const int64_t ku_abs = 4 * t + ku, vu_abs = 4 * t + vu;
     kval = kb >= 0;
-    vhave = vb < 0 ? 0 : (int)min((int64_t)kUnit, most - vu_abs * kUnit);
-    const int ksub = (int)(ku_abs % upp), vsub = (int)(vu_abs % upp);
-    kreg = *reinterpret_cast<const uint4*>(a.k_cache + max(kb, 0) * block +
-                                           (ksub * kUnit + (ktok & 15)) * kHeadDim + 16 * kc);
-    vreg = *reinterpret_cast<const uint4*>(a.v_cache + max(vb, 0) * block +
-                                           (int64_t)vd * a.page_size + vsub * kUnit);
+    vhave = vb < 0 ? 0 : min(kUnit, most - (4 * t + vu) * kUnit);
+    kreg = *reinterpret_cast<const uint4*>(
+        a.k_cache + max(kb, 0) * block +
+        ((((4 * t + ku) & sub) * kUnit + (ktok & 15)) * kHeadDim + 16 * kc));
+    vreg = *reinterpret_cast<const uint4*>(
+        a.v_cache + max(vb, 0) * block + (vd * a.page_size + ((4 * t + vu) & sub) * kUnit));
   };
-  auto store = [&](int buf) {
+  auto store = [&](int buf, int t) {
     // keys: row 8 q + 4 (unit of the 32) + e holds token 4 q + e
     const int i = ktok & 15, m32 = 8 * (i >> 2) + 4 * (ku & 1) + (i & 3);
     const uint4 kx = kval ? kreg : make_uint4(0, 0, 0, 0);
@@ -165,24 +176,36 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     uint4* kp = &lds.k[buf][(ku >> 1) * 8 + kc][m32 ^ ((kc & 1) << 2)];
     kp[0] = __builtin_bit_cast(uint4, codes_bf16x8(kx.x, kx.y));
     kp[32] = __builtin_bit_cast(uint4, codes_bf16x8(kx.z, kx.w));
-    const uint4 vx = vhave == kUnit ? vreg : keep_tokens(vreg, vhave);
+    uint4 vx = vhave == kUnit ? vreg : keep_tokens(vreg, vhave);
+    if ((int64_t)(t + 1) * kTileTok > least) {
+      // A NaN value must reach the rows that see its token and no others, but all rows
+      // share the product, where 0 x NaN is NaN: zero here, and noted.
+      uint32_t word[4] = {vx.x, vx.y, vx.z, vx.w}, mask = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bad = nan_codes(word[e]) >> 7;  // 1 in each NaN byte
+        word[e] &= ~(bad * 0xFFu);
+        // the four flags (bits 0, 8, 16, 24) side by side
+        mask |= ((bad * 0x10204080u) >> 28) << (4 * e);
+      }
+      vx = make_uint4(word[0], word[1], word[2], word[3]);
+      lds.nan_map[buf][vd][vu] = (uint16_t)mask;
+      if (mask != 0) lds.nan_tile[buf] = t + 1;
+    }
     uint4* vp = &lds.v[buf][((vd >> 5) * 2 + (vu >> 1)) * 2][(vu & 1) * 32 + (vd & 31)];
     vp[0] = __builtin_bit_cast(uint4, codes_f16x8(vx.x, vx.y));
     vp[kFrag] = __builtin_bit_cast(uint4, codes_f16x8(vx.z, vx.w));
-    if ((nan_codes(vx.x) | nan_codes(vx.y) | nan_codes(vx.z) | nan_codes(vx.w)) != 0)
-      lds.nan_tile[buf] = 1;
   };
 
-  for (int64_t phase = begin; phase < end; phase += kPhaseTiles) {
+  for (int phase = begin; phase < end; phase += kPhaseTiles) {
     // page data of the next tiles, and the largest value scale so far
-    const int count = (int)min((int64_t)kPhaseTiles, end - phase);
+    const int count = min(kPhaseTiles, end - phase);
     __syncthreads();  // the previous phase has been read
     float vmax = 0.f, vs = 0.f;
-    if (tid < 2) lds.nan_tile[tid] = 0;
     if (tid < kPhaseUnits) {
-      const int64_t u = 4 * phase + tid;
+      const int u = 4 * phase + tid;
       const int blk =
-          tid < 4 * count && u < units ? block_of(a, pages, (int)(u / upp), h) : -1;
+          tid < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
       lds.u_blk[tid] = blk;
       lds.u_ks[tid] = blk < 0 ? 0.f : a.k_scale[blk] * call_scale;
       vs = blk < 0 ? 0.f : a.v_scale[blk];
@@ -204,14 +227,14 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     // value scales below 2^-60 of the largest: fp16 holds nothing of them
     if (tid < kPhaseUnits) lds.u_lv[tid] = vs == vtop ? 0.f : fmaxf(__log2f(vs / vtop), -60.f);
     load(phase, phase);
-    store(0);
+    store(0, phase);
     if (count > 1) load(phase + 1, phase);
 
     for (int c = 0; c < count; ++c) {
       const int buf = c & 1;
       __syncthreads();  // buffer `buf` is written, the other one read
-      const int64_t t = phase + c;
-      if (t * kTileTok < longest) {
+      const int t = phase + c;
+      if (t * kTileTok < longest) {  // (a tile starts below 2^31 - 64)
         at_f32x16 x[2];
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts) {
@@ -223,28 +246,28 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
                 __builtin_bit_cast(at_bf16x8, lds.k[buf][ts * 8 + s][lane ^ ((s & 1) << 2)]), q[s],
                 x[ts], 0, 0, 0);
         }
-        float ksc[2], lv[2];
+        float ksc[2], lv[2], bias[2];
         int have[2];
-        int64_t pos[2];
-        bool whole = true;
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts) {
-          const int i = 4 * c + 2 * ts + half;
+          const int i = 4 * c + 2 * ts + half, pos = (4 * t + 2 * ts + half) * kUnit;
           ksc[ts] = lds.u_ks[i];
           lv[ts] = lds.u_lv[i];
-          pos[ts] = (4 * t + 2 * ts + half) * kUnit;
-          have[ts] = lds.u_blk[i] < 0 ? 0 : (int)min((int64_t)kUnit, max(len - pos[ts], (int64_t)0));
-          whole = whole && have[ts] == kUnit;
+          have[ts] = lds.u_blk[i] < 0 ? 0 : min(kUnit, len - pos);
+          if constexpr (KIND != kPlain) bias[ts] = -slope2 * (float)(len - 1 - pos);
         }
+        const bool whole = have[0] == kUnit && have[1] == kUnit;
         const bool any = !__all(whole);
         float top = -__builtin_inff();
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts) {
-          if constexpr (EXTRA) {
+          if constexpr (KIND != kPlain) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              x[ts][i] = score2<true>(x[ts][i], ksc[ts], a.softcap, slope2,
-                                      (float)(len - 1 - pos[ts] - i));
+            for (int i = 0; i < 16; ++i) {
+              const float c0 = __builtin_fmaf((float)i, slope2, bias[ts]);
+              x[ts][i] = KIND == kCapped ? capped(x[ts][i] * ksc[ts], a.softcap) + c0
+                                         : __builtin_fmaf(x[ts][i], ksc[ts], c0);
+            }
           }
           if (any) {
 #pragma unroll
@@ -254,7 +277,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 #pragma unroll
           for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[ts][i]);
           // a unit without tokens has scale 0: -inf there stays -inf
-          top = fmaxf(top, EXTRA || mx == -__builtin_inff() ? mx : mx * ksc[ts]);
+          top = fmaxf(top, KIND != kPlain || mx == -__builtin_inff() ? mx : mx * ksc[ts]);
         }
         top = halves_max(top);
         if (__any(top > m + kLazy)) {
@@ -271,7 +294,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
         for (int ts = 0; ts < 2; ++ts) {
           const float off = base - kPreBias - lv[ts];
           // not 0, which would make NaN of the masked scores of a unit without tokens
-          const float sc = EXTRA ? 1.f : fmaxf(ksc[ts], 1e-30f);
+          const float sc = KIND != kPlain ? 1.f : fmaxf(ksc[ts], 1e-30f);
           float sum = 0.f;
           uint32_t wd[8];
 #pragma unroll
@@ -285,38 +308,29 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
           p[ts][0] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
           p[ts][1] = make_uint4(wd[4], wd[5], wd[6], wd[7]);
         }
-        const bool nans = any && lds.nan_tile[buf] != 0;
 #pragma unroll
-        for (int dt = 0; dt < 4; ++dt)
+        for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
-          for (int ts = 0; ts < 2; ++ts)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              at_f16x8 vv = __builtin_bit_cast(at_f16x8, lds.v[buf][(dt * 2 + ts) * 2 + e][lane]);
-              if (nans) {
-                // NaN values of tokens that only some rows see: zero in the product, NaN
-                // in the sums of the rows that see them ("is NaN" x "sees" is positive)
-                at_f16x8 is, sees;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const bool bad = vv[j] != vv[j];
-                  is[j] = bad ? (_Float16)1.f : (_Float16)0.f;
-                  vv[j] = bad ? (_Float16)0.f : vv[j];
-                  sees[j] = 8 * e + j < have[ts] ? (_Float16)1.f : (_Float16)0.f;
-                }
-                at_f32x16 hit;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) hit[j] = 0.f;
-                hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(is, sees, hit, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (hit[j] > 0.f) o[dt][j] = __builtin_nanf("");
-              }
+            for (int dt = 0; dt < 4; ++dt)
               o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  vv, __builtin_bit_cast(at_f16x8, p[ts][e]), o[dt], 0, 0, 0);
+                  __builtin_bit_cast(at_f16x8, lds.v[buf][(dt * 2 + ts) * 2 + e][lane]),
+                  __builtin_bit_cast(at_f16x8, p[ts][e]), o[dt], 0, 0, 0);
+        if (lds.nan_tile[buf] == t + 1) {
+          const int seen = min(max(len - t * kTileTok, 0), kTileTok);
+          const uint64_t sees = seen == kTileTok ? ~0ull : (1ull << seen) - 1;
+#pragma unroll
+          for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int d = 32 * dt + 8 * (i >> 2) + 4 * half + (i & 3);
+              const uint64_t bad = *reinterpret_cast<const uint64_t*>(lds.nan_map[buf][d]);
+              if ((bad & sees) != 0) o[dt][i] = __builtin_nanf("");
             }
+        }
       }
-      if (c + 1 < count) store(buf ^ 1);
+      if (c + 1 < count) store(buf ^ 1, t + 1);
       if (c + 2 < count) load(t + 2, phase);
     }
   }
@@ -366,13 +380,14 @@ AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t un
 
 int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool extra = a.softcap > 0.f || a.slopes != nullptr;
   const int64_t tiles = attend_prefill_tiles(a.R, a.B, a.Hq / a.Hkv);
   const dim3 grid((unsigned)(tiles * a.Hkv * sp.splits)), blk(kPreNT);
-#define IDX_PRE(EX)                                                                         \
-  hipLaunchKernelGGL((attend_prefill_kernel<EX>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
+#define IDX_PRE(KIND)                                                                         \
+  hipLaunchKernelGGL((attend_prefill_kernel<KIND>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
                      tiles)
-  if (extra) IDX_PRE(true); else IDX_PRE(false);
+  if (a.softcap > 0.f) IDX_PRE(kCapped);
+  else if (a.slopes != nullptr) IDX_PRE(kBiased);
+  else IDX_PRE(kPlain);
 #undef IDX_PRE
   int e = (int)hipGetLastError();
   if (e == 0 && sp.splits > 1) e = launch_attend_merge(a, sp.splits, stream);
