@@ -2,8 +2,7 @@
 // idx_attend_prefill).
 //
 // A workgroup owns kPreRows rows (token, head of the KV head's group) of one request,
-// 32 to a wave, and walks its tokens in tiles of 64. Bound by the matrix products
-// (512 operations a row and token pair of sums) and the softmax beside them.
+// 32 to a wave, and walks its tokens in tiles of 64.
 //   - The tile's codes are converted once for the workgroup, on their way into LDS:
 //     keys to bf16, values to fp16 (both exact), in the order in which the waves read
 //     them as operands: 1 KB a product, 16 bytes a lane, free of bank conflicts. Two
@@ -20,6 +19,13 @@
 //   - The reference of a row is moved only when its maximum has grown by 2^kLazy or
 //     more (sums are rescaled then); until that, probabilities reach up to 2^kLazy
 //     times 2^kPreBias, which fp16 holds.
+// Two prompts of 8009 and 8192 tokens, 32 heads on 8: 1.15 ms, 0.93 PFLOP/s (a large
+// library product reaches 1.21 on this card); 3.76 ms with 16 rows a product straight from
+// the cache. Bound by the products and the exponentials beside them at the clock the card
+// holds under them, about 2.05 GHz: running the two halves of the waves half a tile apart
+// took 6 to 12 % fewer cycles (4464 against 5079 a tile) at a clock 10 % lower, the same
+// time, and is not done; nor are four waves a workgroup (1.20 ms) or 128 rows straight
+// from registers.
 #include <hip/hip_runtime.h>
 
 #include "attend.hpp"
@@ -34,19 +40,20 @@ namespace {
 constexpr int kPreWaves = 8;
 constexpr int kPreNT = kPreWaves * kWave;
 constexpr int kPreRows = 32 * kPreWaves;
-constexpr int kPhaseTiles = 64;               // tiles whose page data wait in LDS
-constexpr int kPhaseUnits = 4 * kPhaseTiles;
+constexpr int kPreChunk = 512;                // most tiles of a workgroup: page data in LDS
+constexpr int kPreUnits = 4 * (kPreChunk + 4);  // and for the tiles loaded ahead
 constexpr float kPreBias = 9.f;
 constexpr float kLazy = 6.f;
 // what happens to a score beside its scale; capped ones may be biased too
 constexpr int kPlain = 0, kBiased = 1, kCapped = 2;
+constexpr int kAhead = 4;                     // operands read from LDS before their use
 constexpr int kFrag = kWave;                  // uint4s of one operand in LDS
 
 struct PreLds {
   uint4 k[2][16][kFrag];  // [buffer][32-token half, 16-dim step]
   uint4 v[2][16][kFrag];  // [buffer][32-dim tile, 32-token half, 8 tokens of the units]
-  int u_blk[kPhaseUnits];
-  float u_ks[kPhaseUnits], u_lv[kPhaseUnits];
+  int u_blk[kPreUnits];
+  float u_ks[kPreUnits], u_lv[kPreUnits];
   float red[kPreWaves];
   int longest[kPreWaves], shortest[kPreWaves];
   // NaN value codes of a tile that some rows see only in part: which tile (plus one),
@@ -101,7 +108,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   const int64_t rat = min(row, rows - 1);
   const int64_t tok = t0 + rat / G;
   const int hq = h * G + (int)(rat % G);
-  const int len = max(a.kv_len[tok], 0);
+  const int len = row < rows ? max(a.kv_len[tok], 0) : 0;
   const float slope2 = KIND != kPlain ? slope_of(a, hq) : 0.f;
   // dims 16 s + 8 half .. + 7 of the row; a negative call scale turns the queries'
   // signs, so that scores keep their order under the (positive) scale of a unit
@@ -118,7 +125,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   }
   const float call_scale = fabsf(a.score_scale);
 
-  int longest = len, shortest = len;  // of the wave's rows
+  int longest = len, shortest = row < rows ? len : 0x7FFFFFFF;  // of the wave's rows
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     longest = max(longest, __shfl_xor(longest, d));
@@ -137,16 +144,33 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     least = min(least, lds.shortest[i]);
   }
 
-  at_f32x16 o[4];
-#pragma unroll
-  for (int dt = 0; dt < 4; ++dt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
-  float m = -__builtin_inff(), l = 0.f, vref = 0.f;
-
   const int units = min(pages.n << ush, (int)(((int64_t)most + kUnit - 1) / kUnit));
   const int begin = split * chunk;
-  const int end = min((units + 3) / 4, begin + chunk);
+  const int count = min((units + 3) / 4 - begin, chunk);  // tiles of this workgroup
+
+  // page data of the tiles, and the largest value scale
+  float vref = 0.f;
+  for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
+    const int u = 4 * begin + i;
+    const int blk = i < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
+    lds.u_blk[i] = blk;
+    lds.u_ks[i] = blk < 0 ? 0.f : a.k_scale[blk] * call_scale;
+    const float vs = blk < 0 ? 0.f : a.v_scale[blk];
+    lds.u_lv[i] = vs;
+    vref = fmaxf(vref, vs);
+  }
+  vref = halves_max(vref);
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) vref = fmaxf(vref, __shfl_xor(vref, d));
+  if (lane == 0) lds.red[w] = vref;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPreWaves; ++i) vref = fmaxf(vref, lds.red[i]);
+  // value scales as logarithms relative to it; below 2^-60 fp16 holds nothing of them
+  for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
+    const float vs = lds.u_lv[i];
+    lds.u_lv[i] = vs == vref ? 0.f : fmaxf(__log2f(vs / vref), -60.f);
+  }
 
   // staging: thread -> (token, 16 dims) of the keys and (unit, dim) of the values
   const int64_t block = (int64_t)a.page_size * kHeadDim;
@@ -157,30 +181,34 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   uint4 kreg, vreg;
   int vhave = 0;  // visible tokens of this thread's value unit
   bool kval = false;
-  auto load = [&](int t, int phase) {
-    const int i = (t - phase) * 4;
-    const int kb = lds.u_blk[i + ku], vb = lds.u_blk[i + vu];
+  auto load_k = [&](int c) {  // c: tile of the workgroup
+    const int kb = lds.u_blk[4 * c + ku];
     kval = kb >= 0;
-    vhave = vb < 0 ? 0 : min(kUnit, most - (4 * t + vu) * kUnit);
     kreg = *reinterpret_cast<const uint4*>(
         a.k_cache + max(kb, 0) * block +
-        ((((4 * t + ku) & sub) * kUnit + (ktok & 15)) * kHeadDim + 16 * kc));
-    vreg = *reinterpret_cast<const uint4*>(
-        a.v_cache + max(vb, 0) * block + (vd * a.page_size + ((4 * t + vu) & sub) * kUnit));
+        ((((4 * (begin + c) + ku) & sub) * kUnit + (ktok & 15)) * kHeadDim + 16 * kc));
   };
-  auto store = [&](int buf, int t) {
-    // keys: row 8 q + 4 (unit of the 32) + e holds token 4 q + e
+  auto load_v = [&](int c) {
+    const int vb = lds.u_blk[4 * c + vu], u = 4 * (begin + c) + vu;
+    vhave = vb < 0 ? 0 : min(kUnit, most - u * kUnit);
+    vreg = *reinterpret_cast<const uint4*>(a.v_cache + max(vb, 0) * block +
+                                           (vd * a.page_size + (u & sub) * kUnit));
+  };
+  auto store_k = [&](int c) {
+    // row 8 q + 4 (unit of the 32) + e holds token 4 q + e; every other step swaps rows 4
+    // apart, so that 16 lanes' stores meet 16 different banks of 16 bytes
     const int i = ktok & 15, m32 = 8 * (i >> 2) + 4 * (ku & 1) + (i & 3);
-    const uint4 kx = kval ? kreg : make_uint4(0, 0, 0, 0);
-    // every other step swaps rows 4 apart, so that 16 lanes' stores meet 16 banks of 16
-    uint4* kp = &lds.k[buf][(ku >> 1) * 8 + kc][m32 ^ ((kc & 1) << 2)];
-    kp[0] = __builtin_bit_cast(uint4, codes_bf16x8(kx.x, kx.y));
-    kp[32] = __builtin_bit_cast(uint4, codes_bf16x8(kx.z, kx.w));
-    uint4 vx = vhave == kUnit ? vreg : keep_tokens(vreg, vhave);
-    if ((int64_t)(t + 1) * kTileTok > least) {
+    const uint4 x = kval ? kreg : make_uint4(0, 0, 0, 0);
+    uint4* p = &lds.k[c & 1][(ku >> 1) * 8 + kc][m32 ^ ((kc & 1) << 2)];
+    p[0] = __builtin_bit_cast(uint4, codes_bf16x8(x.x, x.y));
+    p[32] = __builtin_bit_cast(uint4, codes_bf16x8(x.z, x.w));
+  };
+  auto store_v = [&](int c) {
+    uint4 x = vhave == kUnit ? vreg : keep_tokens(vreg, vhave);
+    if ((int64_t)(begin + c + 1) * kTileTok > least) {
       // A NaN value must reach the rows that see its token and no others, but all rows
       // share the product, where 0 x NaN is NaN: zero here, and noted.
-      uint32_t word[4] = {vx.x, vx.y, vx.z, vx.w}, mask = 0;
+      uint32_t word[4] = {x.x, x.y, x.z, x.w}, mask = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t bad = nan_codes(word[e]) >> 7;  // 1 in each NaN byte
@@ -188,150 +216,170 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
         // the four flags (bits 0, 8, 16, 24) side by side
         mask |= ((bad * 0x10204080u) >> 28) << (4 * e);
       }
-      vx = make_uint4(word[0], word[1], word[2], word[3]);
-      lds.nan_map[buf][vd][vu] = (uint16_t)mask;
-      if (mask != 0) lds.nan_tile[buf] = t + 1;
+      x = make_uint4(word[0], word[1], word[2], word[3]);
+      lds.nan_map[c & 1][vd][vu] = (uint16_t)mask;
+      if (mask != 0) lds.nan_tile[c & 1] = c + 1;
     }
-    uint4* vp = &lds.v[buf][((vd >> 5) * 2 + (vu >> 1)) * 2][(vu & 1) * 32 + (vd & 31)];
-    vp[0] = __builtin_bit_cast(uint4, codes_f16x8(vx.x, vx.y));
-    vp[kFrag] = __builtin_bit_cast(uint4, codes_f16x8(vx.z, vx.w));
+    uint4* p = &lds.v[c & 1][((vd >> 5) * 2 + (vu >> 1)) * 2][(vu & 1) * 32 + (vd & 31)];
+    p[0] = __builtin_bit_cast(uint4, codes_f16x8(x.x, x.y));
+    p[kFrag] = __builtin_bit_cast(uint4, codes_f16x8(x.z, x.w));
   };
 
-  for (int phase = begin; phase < end; phase += kPhaseTiles) {
-    // page data of the next tiles, and the largest value scale so far
-    const int count = min(kPhaseTiles, end - phase);
-    __syncthreads();  // the previous phase has been read
-    float vmax = 0.f, vs = 0.f;
-    if (tid < kPhaseUnits) {
-      const int u = 4 * phase + tid;
-      const int blk =
-          tid < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
-      lds.u_blk[tid] = blk;
-      lds.u_ks[tid] = blk < 0 ? 0.f : a.k_scale[blk] * call_scale;
-      vs = blk < 0 ? 0.f : a.v_scale[blk];
-      vmax = halves_max(vs);
+  // the wave's state
+  at_f32x16 o[4];
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2) vmax = fmaxf(vmax, __shfl_xor(vmax, d));
-      if (lane == 0) lds.red[w] = vmax;
+  for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+  float m = -__builtin_inff(), l = 0.f;
+  float ksc[2], lv[2];  // scales of the tile
+  const int mine = (int)min((int64_t)count, ((int64_t)longest + kTileTok - 1) / kTileTok - begin);
+
+  // operands are read from LDS kAhead products before their use
+  auto products = [&](at_f32x16 (&x)[2], int c) {
+    auto read = [&](int i) {
+      return __builtin_bit_cast(at_bf16x8, lds.k[c & 1][i][lane ^ ((i & 1) << 2)]);
+    };
+    at_bf16x8 f[16];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = read(i);
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[ts][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + kAhead < 16) f[i + kAhead] = read(i + kAhead);
+      x[i >> 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i], q[i & 7], x[i >> 3], 0, 0, 0);
     }
-    __syncthreads();
-    float vtop = vref;
+    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-    for (int i = 0; i < kPhaseUnits / kWave; ++i) vtop = fmaxf(vtop, lds.red[i]);
-    if (vtop > vref) {
-      const float f = vref / vtop;
+    for (int i = 0; i < 16; ++i) {
+      if (i + kAhead < 16) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+  };
+  // maxima, masks and the reference of tile c, whose products are in x
+  auto reference = [&](at_f32x16 (&x)[2], int c) {
+    int have[2];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      const int i = 4 * c + 2 * ts + half, pos = (4 * begin + i) * kUnit;
+      ksc[ts] = lds.u_ks[i];
+      lv[ts] = lds.u_lv[i];
+      have[ts] = lds.u_blk[i] < 0 ? 0 : min(kUnit, len - pos);
+      if constexpr (KIND != kPlain) {
+        const float bias = -slope2 * (float)(len - 1 - pos);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float c0 = __builtin_fmaf((float)j, slope2, bias);
+          x[ts][j] = KIND == kCapped ? capped(x[ts][j] * ksc[ts], a.softcap) + c0
+                                     : __builtin_fmaf(x[ts][j], ksc[ts], c0);
+        }
+        ksc[ts] = 1.f;
+      }
+      float mx = x[ts][0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) mx = fmaxf(mx, x[ts][j]);
+      top = fmaxf(top, mx * ksc[ts]);
+    }
+    if (__any(have[0] < kUnit || have[1] < kUnit)) {
+      top = -__builtin_inff();
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        // not 0, which would make NaN of the masked scores of a unit without tokens
+        ksc[ts] = fmaxf(ksc[ts], 1e-30f);
+        float mx = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          x[ts][j] = j < have[ts] ? x[ts][j] : -__builtin_inff();
+          mx = fmaxf(mx, x[ts][j]);
+        }
+        top = fmaxf(top, mx * ksc[ts]);
+      }
+    }
+    top = halves_max(top);
+    if (__any(top > m + kLazy)) {
+      const float mn = fmaxf(m, top);
+      const float f = exp2_fast(m - (mn == -__builtin_inff() ? 0.f : mn));
+      m = mn;
+      l *= f;
 #pragma unroll
       for (int dt = 0; dt < 4; ++dt) o[dt] *= f;
-      vref = vtop;
     }
-    // value scales below 2^-60 of the largest: fp16 holds nothing of them
-    if (tid < kPhaseUnits) lds.u_lv[tid] = vs == vtop ? 0.f : fmaxf(__log2f(vs / vtop), -60.f);
-    load(phase, phase);
-    store(0, phase);
-    if (count > 1) load(phase + 1, phase);
-
-    for (int c = 0; c < count; ++c) {
-      const int buf = c & 1;
-      __syncthreads();  // buffer `buf` is written, the other one read
-      const int t = phase + c;
-      if (t * kTileTok < longest) {  // (a tile starts below 2^31 - 64)
-        at_f32x16 x[2];
+  };
+  auto step = [&](int c) {
+    at_f32x16 x[2];
+    products(x, c);
+    __builtin_amdgcn_sched_barrier(0);
+    reference(x, c);
+    auto read = [&](int i) {  // 8 tokens a quarter, dims 32 (i % 4) ..
+      return __builtin_bit_cast(at_f16x8, lds.v[c & 1][(i & 3) * 4 + (i >> 2)][lane]);
+    };
+    at_f16x8 f[16];
 #pragma unroll
-        for (int ts = 0; ts < 2; ++ts) {
+    for (int i = 0; i < kAhead; ++i) f[i] = read(i);
+    const float base = m == -__builtin_inff() ? 0.f : m;
+    uint4 p[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[ts][i] = 0.f;
+    for (int ts = 0; ts < 2; ++ts) {
+      const float off = base - kPreBias - lv[ts];
+      float sum = 0.f;
+      uint32_t wd[8];
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            x[ts] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(at_bf16x8, lds.k[buf][ts * 8 + s][lane ^ ((s & 1) << 2)]), q[s],
-                x[ts], 0, 0, 0);
-        }
-        float ksc[2], lv[2], bias[2];
-        int have[2];
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts) {
-          const int i = 4 * c + 2 * ts + half, pos = (4 * t + 2 * ts + half) * kUnit;
-          ksc[ts] = lds.u_ks[i];
-          lv[ts] = lds.u_lv[i];
-          have[ts] = lds.u_blk[i] < 0 ? 0 : min(kUnit, len - pos);
-          if constexpr (KIND != kPlain) bias[ts] = -slope2 * (float)(len - 1 - pos);
-        }
-        const bool whole = have[0] == kUnit && have[1] == kUnit;
-        const bool any = !__all(whole);
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts) {
-          if constexpr (KIND != kPlain) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float c0 = __builtin_fmaf((float)i, slope2, bias[ts]);
-              x[ts][i] = KIND == kCapped ? capped(x[ts][i] * ksc[ts], a.softcap) + c0
-                                         : __builtin_fmaf(x[ts][i], ksc[ts], c0);
-            }
-          }
-          if (any) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[ts][i] = i < have[ts] ? x[ts][i] : -__builtin_inff();
-          }
-          float mx = x[ts][0];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[ts][i]);
-          // a unit without tokens has scale 0: -inf there stays -inf
-          top = fmaxf(top, KIND != kPlain || mx == -__builtin_inff() ? mx : mx * ksc[ts]);
-        }
-        top = halves_max(top);
-        if (__any(top > m + kLazy)) {
-          const float mn = fmaxf(m, top);
-          const float f = exp2_fast(m - (mn == -__builtin_inff() ? 0.f : mn));
-          m = mn;
-          l *= f;
-#pragma unroll
-          for (int dt = 0; dt < 4; ++dt) o[dt] *= f;
-        }
-        const float base = m == -__builtin_inff() ? 0.f : m;
-        uint4 p[2][2];
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts) {
-          const float off = base - kPreBias - lv[ts];
-          // not 0, which would make NaN of the masked scores of a unit without tokens
-          const float sc = KIND != kPlain ? 1.f : fmaxf(ksc[ts], 1e-30f);
-          float sum = 0.f;
-          uint32_t wd[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float e0 = exp2_fast(__builtin_fmaf(x[ts][2 * i], sc, -off));
-            const float e1 = exp2_fast(__builtin_fmaf(x[ts][2 * i + 1], sc, -off));
-            sum += e0 + e1;
-            wd[i] = pack_f16(e0, e1);
-          }
-          l = __builtin_fmaf(sum, exp2_fast(-lv[ts]), l);
-          p[ts][0] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-          p[ts][1] = make_uint4(wd[4], wd[5], wd[6], wd[7]);
-        }
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int dt = 0; dt < 4; ++dt)
-              o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  __builtin_bit_cast(at_f16x8, lds.v[buf][(dt * 2 + ts) * 2 + e][lane]),
-                  __builtin_bit_cast(at_f16x8, p[ts][e]), o[dt], 0, 0, 0);
-        if (lds.nan_tile[buf] == t + 1) {
-          const int seen = min(max(len - t * kTileTok, 0), kTileTok);
-          const uint64_t sees = seen == kTileTok ? ~0ull : (1ull << seen) - 1;
-#pragma unroll
-          for (int dt = 0; dt < 4; ++dt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int d = 32 * dt + 8 * (i >> 2) + 4 * half + (i & 3);
-              const uint64_t bad = *reinterpret_cast<const uint64_t*>(lds.nan_map[buf][d]);
-              if ((bad & sees) != 0) o[dt][i] = __builtin_nanf("");
-            }
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float e0 = exp2_fast(__builtin_fmaf(x[ts][2 * i], ksc[ts], -off));
+        const float e1 = exp2_fast(__builtin_fmaf(x[ts][2 * i + 1], ksc[ts], -off));
+        sum += e0 + e1;
+        wd[i] = pack_f16(e0, e1);
       }
-      if (c + 1 < count) store(buf ^ 1, t + 1);
-      if (c + 2 < count) load(t + 2, phase);
+      l = __builtin_fmaf(sum, exp2_fast(-lv[ts]), l);
+      p[2 * ts] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+      p[2 * ts + 1] = make_uint4(wd[4], wd[5], wd[6], wd[7]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + kAhead < 16) f[i + kAhead] = read(i + kAhead);
+      o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          f[i], __builtin_bit_cast(at_f16x8, p[i >> 2]), o[i & 3], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + kAhead < 16) __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (lds.nan_tile[c & 1] == c + 1) {
+      const int seen = min(max(len - (begin + c) * kTileTok, 0), kTileTok);
+      const uint64_t sees = seen == kTileTok ? ~0ull : (1ull << seen) - 1;
+#pragma unroll
+      for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int d = 32 * dt + 8 * (i >> 2) + 4 * half + (i & 3);
+          const uint64_t bad = *reinterpret_cast<const uint64_t*>(lds.nan_map[c & 1][d]);
+          if ((bad & sees) != 0) o[dt][i] = __builtin_nanf("");
+          __builtin_amdgcn_sched_barrier(0);  // a rare path: no registers for it
+        }
+    }
+  };
+
+  if (count > 0) {
+    load_k(0);
+    load_v(0);
+    store_k(0);
+    store_v(0);
+    load_k(1);
+    load_v(1);
+    for (int c = 0; c < count; ++c) {
+      __syncthreads();  // tile c is written, tile c - 1 read
+      if (c < mine) step(c);
+      store_k(c + 1);
+      store_v(c + 1);
+      load_k(c + 2);
+      load_v(c + 2);
     }
   }
 
@@ -368,13 +416,23 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 
 int64_t attend_prefill_tiles(int64_t n_tok, int B, int G) { return n_tok * G / kPreRows + B; }
 
+// A long context is cut so that about 512 workgroups share the call, but not below 32 tiles
+// each (a workgroup's start, and its partial sums, written and read again, cost about five
+// tiles' time: chunks of 512 tokens on 4608 and 30512, 32 heads on 8, took 486 us at 512
+// workgroups wanted, 513 at 1024, 520 at 1536); a call of few workgroups into as many as
+// there are CUs, down to four tiles (five tokens on 900 to 2777: 29 us before, 22 so).
 AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
   const int64_t tiles = (units + 3) / 4;
   const int64_t groups = attend_prefill_tiles(n_tok, B, Hq / Hkv) * Hkv;
-  int64_t splits = (512 + groups - 1) / groups;
-  splits = splits < tiles / 8 ? splits : tiles / 8;
-  if (splits < 1) splits = 1;
-  const int64_t chunk = (tiles + splits - 1) / splits;
+  auto most = [&](int64_t want, int64_t least) {
+    const int64_t s = (want + groups - 1) / groups, t = tiles / least;
+    return s < t ? s : t;
+  };
+  int64_t splits = 1;
+  if (most(256, 4) > splits) splits = most(256, 4);
+  if (most(512, 32) > splits) splits = most(512, 32);
+  int64_t chunk = (tiles + splits - 1) / splits;
+  if (chunk > kPreChunk) chunk = kPreChunk;
   return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
 }
 
