@@ -8,11 +8,11 @@
 //   served       need == 0 or N_b <= free
 //   pages held   P_b = sum_{b'<b} ceil(after/page), pages given back G_b likewise.
 // A request's outputs then need only its own prefixes, so every workgroup runs
-// the sums over all requests for itself (the lengths are a few KB, in L2) and
-// fills the lists of its own requests: one launch, no workspace, no atomics, and
-// nothing that depends on the order in which workgroups run. New pages come from
-// the ring in front of the free count, pages given back go behind it, so no
-// workgroup writes an entry that another reads.
+// the sums over all requests for itself (the lengths are a few KB, in L2; a thread holds
+// up to 16 requests in registers) and fills the lists of its own requests: one launch,
+// no workspace, no atomics, and nothing that depends on the order in which workgroups
+// run. New pages come from the ring in front of the free count, pages given back go
+// behind it, so no workgroup writes an entry that another reads.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -22,156 +22,162 @@ namespace idxk {
 
 namespace {
 
-constexpr int kTabNT = 256;
-constexpr int kTabWaves = kTabNT / kWave;
-constexpr int kTabOwn = 16;  // most requests of one workgroup
+constexpr int kTabOwn = 64;  // most requests of one workgroup
 
 struct TabReq {
-  int64_t have, after;  // tokens before and after the step
   int64_t tok;          // first token row
+  int have, after;      // tokens before and after the step
   int old_pages, new_pages;
   int grown, gave;      // first new page, first page given back
   int kv;               // first entry in kv_indices
-  int fresh;            // token rows
+  int fresh;            // token rows (at most n_tok)
   bool served;
 };
 
-// inclusive prefix sum over the workgroup of one value per thread; `total` gets
-// the sum
-__device__ int64_t block_scan(int64_t v, int64_t* lds, int64_t& total) {
+// Exclusive prefix sums over the workgroup's threads of N values at once; v becomes the
+// sum of the threads before, total that of all.
+template <int NT, int N, typename T>
+__device__ __forceinline__ void block_scan(T (&v)[N], T (*lds)[NT / kWave], T (&total)[N]) {
   const int lane = lane_id(), w = threadIdx.x / kWave;
+  T own[N];
 #pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int64_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();  // the previous scan's sums have been read
-  if (lane == kWave - 1) lds[w] = v;
+  for (int i = 0; i < N; ++i) own[i] = v[i];
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const T o = __shfl_up(v[i], d);
+      if (lane >= d) v[i] += o;
+    }
+  __syncthreads();  // the previous sums have been read
+  if (lane == kWave - 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[i][w] = v[i];
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
 #pragma unroll
-  for (int i = 0; i < kTabWaves; ++i) {
-    const int64_t s = lds[i];
-    before += i < w ? s : 0;
-    total += s;
+  for (int i = 0; i < N; ++i) {
+    T before = 0;
+    total[i] = 0;
+#pragma unroll
+    for (int j = 0; j < NT / kWave; ++j) {
+      const T s = lds[i][j];
+      before += j < w ? s : 0;
+      total[i] += s;
+    }
+    v[i] += before - own[i];
   }
-  return v + before;
 }
 
-__global__ __launch_bounds__(kTabNT) void page_tables_kernel(
+// NT threads, PER requests a thread (NT * PER >= B).
+template <int NT, int PER>
+__global__ __launch_bounds__(NT) void page_tables_kernel(
     const int32_t* __restrict__ seq_len, const int32_t* __restrict__ n_new,
     const int32_t* __restrict__ cursor, int32_t* table, int32_t* ring,
     int32_t* __restrict__ seq_out, int32_t* __restrict__ cursor_out,
     int32_t* __restrict__ kv_indptr, int32_t* __restrict__ kv_indices,
     int32_t* __restrict__ tok_indptr, int32_t* __restrict__ slots,
     int32_t* __restrict__ tok_req, int32_t* __restrict__ tok_len, int B, int max_pages,
-    int page_size, int n_pages, int64_t n_indices, int n_tok, int own, int per_thread) {
-  __shared__ int64_t lds[kTabWaves];
+    int page_size, int n_pages, int64_t n_indices, int n_tok, int own,
+    int shift) {
+  __shared__ int64_t lds64[1][NT / kWave];
+  __shared__ int lds32[4][NT / kWave];
   __shared__ TabReq mine[kTabOwn];
   const int tid = threadIdx.x;
   const int b0 = blockIdx.x * own, b1 = min(b0 + own, B);
-  const int64_t most = (int64_t)max_pages * page_size;
-  const int64_t head = (((int64_t)cursor[0] % n_pages) + n_pages) % n_pages;
-  const int64_t free_n = min(max((int64_t)cursor[1], (int64_t)0), (int64_t)n_pages);
+  const int most = max_pages * page_size;
 
-  // this thread's requests: per_thread consecutive ones
-  const int first = tid * per_thread, last = min(first + per_thread, B);
-  auto load = [&](int b, int64_t& have, int64_t& after, int64_t& fresh) {
-    have = min(max((int64_t)seq_len[b], (int64_t)0), most);
-    const int64_t d = n_new[b];
-    after = max(have + d, (int64_t)0);
-    fresh = max(d, (int64_t)0);
+  // this thread's requests: PER consecutive ones
+  int have[PER], change[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    have[i] = b < B ? min(max(seq_len[b], 0), most) : 0;
+    change[i] = b < B ? n_new[b] : 0;
+  }
+  const int head = ((cursor[0] % n_pages) + n_pages) % n_pages;
+  const int free_n = min(max(cursor[1], 0), n_pages);
+  // division by page_size, a shift where it is a power of two
+  auto div = [&](uint32_t x) {
+    return (int)(shift >= 0 ? x >> shift : x / (uint32_t)page_size);
   };
-  auto pages = [&](int64_t tokens) { return (tokens + page_size - 1) / page_size; };
+  auto pages = [&](int tokens) { return div((uint32_t)tokens + (page_size - 1)); };
 
-  int64_t have, after, fresh, total_tok, total_need, total_pages, total_gave, n_refused;
-  int64_t tok = 0;
-  for (int b = first; b < last; ++b) {
-    load(b, have, after, fresh);
-    tok += fresh;
+  int64_t tok[1] = {0}, total_tok[1];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) tok[0] += max(change[i], 0);
+  block_scan<NT>(tok, lds64, total_tok);
+
+  // pages needed; -1 marks a request that cannot be served whatever is free
+  int need[PER], sum[1] = {0}, total_need[1];
+  int64_t t = tok[0];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    t += max(change[i], 0);
+    const int64_t after = max((int64_t)have[i] + change[i], (int64_t)0);
+    const bool fits = after <= most && (change[i] <= 0 || t <= n_tok);
+    need[i] = fits ? max(pages((int)after) - pages(have[i]), 0) : -1;
+    sum[0] += max(need[i], 0);
   }
-  tok = block_scan(tok, lds, total_tok) - tok;  // before this thread's requests
-  // pages needed by request b, whose token rows end at row `end`
-  auto need_of = [&](int64_t end, bool& fits) {
-    fits = after <= most && (fresh == 0 || end <= n_tok);
-    return fits ? max(pages(after) - pages(have), (int64_t)0) : (int64_t)0;
+  block_scan<NT>(sum, lds32, total_need);
+
+  int v[4] = {0, 0, 0, 0}, total[4];  // pages held, given back, taken; requests refused
+  int n = sum[0];
+  auto step = [&](int i, int& after, int& np) {  // whether request i is served
+    n += max(need[i], 0);
+    const bool served = need[i] == 0 || (need[i] > 0 && n <= free_n);
+    after = served ? (int)max((int64_t)have[i] + change[i], (int64_t)0) : have[i];
+    np = pages(after);
+    return served;
   };
-  int64_t need = 0, t = tok;
-  bool fits;
-  for (int b = first; b < last; ++b) {
-    load(b, have, after, fresh);
-    t += fresh;
-    need += need_of(t, fits);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    int after, np;
+    const bool served = step(i, after, np);
+    v[0] += np;
+    v[1] += max(pages(have[i]) - np, 0);
+    v[2] += served ? need[i] : 0;
+    v[3] += !served && tid * PER + i < B ? 1 : 0;
   }
-  need = block_scan(need, lds, total_need) - need;
-  int64_t held = 0, gave = 0, refused = 0, taken = 0, n = need;
-  t = tok;
-  for (int b = first; b < last; ++b) {
-    load(b, have, after, fresh);
-    t += fresh;
-    const int64_t k = need_of(t, fits);
-    n += k;
-    const bool served = fits && (k == 0 || n <= free_n);
-    const int64_t np = pages(served ? after : have);
-    held += np;
-    gave += max(pages(have) - np, (int64_t)0);
-    taken += served ? k : 0;
-    refused += served ? 0 : 1;
-  }
-  int64_t total_taken;
-  const int64_t held0 = block_scan(held, lds, total_pages) - held;
-  const int64_t gave0 = block_scan(gave, lds, total_gave) - gave;
-  block_scan(taken, lds, total_taken);
-  block_scan(refused, lds, n_refused);
+  block_scan<NT>(v, lds32, total);
 
   // the prefixes of this workgroup's own requests
-  if (first < b1 && last > b0) {
-    t = tok;
-    n = need;
-    int64_t h = held0, g = gave0;
-    for (int b = first; b < last; ++b) {
-      load(b, have, after, fresh);
-      const int64_t t0 = t;
-      t += fresh;
-      const int64_t k = need_of(t, fits);
-      const bool served = fits && (k == 0 || n + k <= free_n);
-      const int64_t np = pages(served ? after : have);
-      if (b >= b0 && b < b1) {
-        TabReq& r = mine[b - b0];
-        r.have = have;
-        r.after = served ? after : have;
-        r.tok = t0;
-        r.old_pages = (int)pages(have);
-        r.new_pages = (int)np;
-        r.grown = (int)n;
-        r.gave = (int)g;
-        r.kv = (int)h;
-        r.fresh = (int)min(fresh, (int64_t)n_tok);
-        r.served = served;
-      }
-      n += k;
-      h += np;
-      g += max(pages(have) - np, (int64_t)0);
+  if (tid * PER < b1 && (tid + 1) * PER > b0) {
+    t = tok[0];
+    n = sum[0];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = tid * PER + i, grown = n;
+      int after, np;
+      const bool served = step(i, after, np);
+      if (b >= b0 && b < b1)
+        mine[b - b0] = TabReq{t,     have[i], after, pages(have[i]), np, grown, v[1], v[0],
+                              (int)min((int64_t)max(change[i], 0), (int64_t)n_tok), served};
+      t += max(change[i], 0);
+      v[0] += np;
+      v[1] += max(pages(have[i]) - np, 0);
     }
   }
   __syncthreads();
 
-  const bool lead = blockIdx.y == 0;  // writes the per-request words
-  for (int b = b0; b < b1; ++b) {
-    const TabReq r = mine[b - b0];
+  // a wave fills a request's lists; the whole workgroup (and gridDim.y of them) if it
+  // has one request only
+  const int team = own > 1 ? kWave : NT;
+  const int at0 = blockIdx.y * team + tid % team, step_n = gridDim.y * team;
+  const bool lead = blockIdx.y == 0 && tid % team == 0;  // writes the per-request words
+  for (int k = tid / team; k < b1 - b0; k += NT / team) {
+    const TabReq r = mine[k];
+    const int b = b0 + k;
     int32_t* row = table + (int64_t)b * max_pages;
-    // page of list entry i: held before, or taken from the ring in this step
-    auto fresh_page = [&](int i) {
-      return ring[(head + r.grown + (i - r.old_pages)) % n_pages];
+    // a page taken from the ring in this step
+    auto new_page = [&](int i) {
+      return ring[((int64_t)head + r.grown + (i - r.old_pages)) % n_pages];
     };
-    const int step = gridDim.y * kTabNT;
-    for (int i = blockIdx.y * kTabNT + tid; i < r.new_pages; i += step) {
+    for (int i = at0; i < r.new_pages; i += step_n) {
       int32_t p;
       if (i < r.old_pages) {
         p = row[i];
       } else {
-        p = fresh_page(i);
+        p = new_page(i);
         row[i] = p;
       }
       const int64_t at = (int64_t)r.kv + i;
@@ -179,50 +185,46 @@ __global__ __launch_bounds__(kTabNT) void page_tables_kernel(
     }
     // pages given back join the ring behind the free ones (more than the ring has
     // room for can only come from an inconsistent state: they are dropped)
-    for (int i = r.new_pages + blockIdx.y * kTabNT + tid; i < r.old_pages; i += step) {
-      const int64_t j = free_n + r.gave + (i - r.new_pages);
+    for (int i = r.new_pages + at0; i < r.old_pages; i += step_n) {
+      const int64_t j = (int64_t)free_n + r.gave + (i - r.new_pages);
       if (j < n_pages) ring[(head + j) % n_pages] = row[i];
     }
-    for (int64_t i = blockIdx.y * kTabNT + tid; i < r.fresh; i += step) {
+    for (int i = at0; i < r.fresh; i += step_n) {
       const int64_t at = r.tok + i;
       if (at >= n_tok) break;
       int32_t slot = -1, len = 0;
       if (r.served) {
-        const int64_t pos = r.have + i;
-        const int e = (int)(pos / page_size);
-        const int32_t p = e < r.old_pages ? row[e] : fresh_page(e);
+        const int pos = r.have + i, e = div((uint32_t)pos);
+        const int32_t p = e < r.old_pages ? row[e] : new_page(e);
         if (p >= 0 && p < n_pages) {  // else: not an entry that a step handed out
-          slot = p * page_size + (int)(pos % page_size);
-          len = (int)pos + 1;
+          slot = p * page_size + (pos - e * page_size);
+          len = pos + 1;
         }
       }
       slots[at] = slot;
       tok_req[at] = b;
       tok_len[at] = len;
     }
-    if (lead && tid == 0) {
-      seq_out[b] = (int32_t)r.after;
+    if (lead) {
+      seq_out[b] = r.after;
       kv_indptr[b] = r.kv;
       tok_indptr[b] = (int32_t)min(r.tok, (int64_t)n_tok);
-      if (b == B - 1) {
-        kv_indptr[B] = (int32_t)total_pages;
-        tok_indptr[B] = (int32_t)min(total_tok, (int64_t)n_tok);
-      }
     }
   }
-  // the rows past the last token
-  if (blockIdx.x == gridDim.x - 1) {
-    for (int64_t i = min(total_tok, (int64_t)n_tok) + blockIdx.y * kTabNT + tid; i < n_tok;
-         i += gridDim.y * kTabNT) {
+  // the rows past the last token, and what belongs to no request
+  if (blockIdx.x == gridDim.x - 1)
+    for (int64_t i = min(total_tok[0], (int64_t)n_tok) + blockIdx.y * NT + tid; i < n_tok;
+         i += gridDim.y * NT) {
       slots[i] = -1;
       tok_req[i] = -1;
       tok_len[i] = 0;
     }
-  }
-  if (blockIdx.x == 0 && lead && tid == 0) {
-    cursor_out[0] = (int32_t)((head + total_taken) % n_pages);
-    cursor_out[1] = (int32_t)min(free_n - total_taken + total_gave, (int64_t)n_pages);
-    cursor_out[2] = (int32_t)n_refused;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    kv_indptr[B] = total[0];
+    tok_indptr[B] = (int32_t)min(total_tok[0], (int64_t)n_tok);
+    cursor_out[0] = (int32_t)(((int64_t)head + total[2]) % n_pages);
+    cursor_out[1] = (int32_t)min((int64_t)free_n - total[2] + total[1], (int64_t)n_pages);
+    cursor_out[2] = total[3];
   }
 }
 
@@ -233,16 +235,27 @@ int launch_page_tables(const int32_t* seq_len, const int32_t* n_new, const int32
                        int32_t* kv_indptr, int32_t* kv_indices, int32_t* tok_indptr,
                        int32_t* slots, int32_t* tok_req, int32_t* tok_len, int B, int max_pages,
                        int page_size, int n_pages, int64_t n_indices, int n_tok, void* stream) {
-  const int own = (B + 1023) / 1024;  // at most kTabOwn for B <= 16384
+  // up to 256 requests: one thread and one workgroup (or several) for each; more: a
+  // wave for each, 256 workgroups running the sums (4096 requests: 65 us with a
+  // workgroup of 256 threads for each four, which reread the lengths, 16.6 so)
+  const int own = B <= 256 ? 1 : (B + 255) / 256;
   const int gx = (B + own - 1) / own;
   int gy = 1;  // a few requests: several workgroups for each
   const int64_t longest = (max_pages > n_tok ? max_pages : n_tok);
-  while (gy < 16 && gx * gy < 256 && (int64_t)gy * kTabNT < longest) gy *= 2;
-  hipLaunchKernelGGL(page_tables_kernel, dim3(gx, gy), dim3(kTabNT), 0,
-                     static_cast<hipStream_t>(stream), seq_len, n_new, cursor, table, ring,
-                     seq_out, cursor_out, kv_indptr, kv_indices, tok_indptr, slots, tok_req,
-                     tok_len, B, max_pages, page_size, n_pages, n_indices, n_tok, own,
-                     (B + kTabNT - 1) / kTabNT);
+  while (gy < 16 && gx * gy < 256 && (int64_t)gy * 256 < longest) gy *= 2;
+  int shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) shift = i;
+#define IDX_TABLES(NT, PER)                                                                      \
+  hipLaunchKernelGGL((page_tables_kernel<NT, PER>), dim3(gx, gy), dim3(NT), 0,                   \
+                     static_cast<hipStream_t>(stream), seq_len, n_new, cursor, table, ring,      \
+                     seq_out, cursor_out, kv_indptr, kv_indices, tok_indptr, slots, tok_req,     \
+                     tok_len, B, max_pages, page_size, n_pages, n_indices, n_tok, own, shift)
+  if (B <= 256) IDX_TABLES(256, 1);
+  else if (B <= 1024) IDX_TABLES(1024, 1);
+  else if (B <= 4096) IDX_TABLES(1024, 4);
+  else IDX_TABLES(1024, 16);
+#undef IDX_TABLES
   return (int)hipGetLastError();
 }
 
