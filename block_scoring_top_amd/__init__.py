@@ -8,6 +8,7 @@ kernels; there is no fallback path. PyTorch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -402,28 +403,42 @@ class PageTables(NamedTuple):
     tok_len: torch.Tensor      # [n_tokens] position + 1, 0: none
 
 
-def _int32(**ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
+# The calls below are short kernels next to decode steps: their checks touch each tensor
+# once, and the outputs of one call share an allocation.
+
+_I32 = torch.int32
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-class _on:
-    """Makes a tensor's device the current one for the call (the kernels run on the
-    current device); nothing to do, and no cost, when it is already."""
+def _words(dev, *ts):
+    """Every given tensor is a contiguous int32 one on `dev`."""
+    for t in ts:
+        if t is not None:
+            if t.device != dev:
+                raise ValueError("all tensors must live on the same GPU")
+            if t.dtype is not _I32:
+                raise TypeError("index, length and pointer tensors must be int32")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
 
-    def __init__(self, dev):
-        self.dev = dev
 
-    def __enter__(self):
-        index = torch.cuda.current_device()
-        self.back = None if self.dev.index == index else index
-        if self.back is not None:
-            torch.cuda.set_device(self.dev)
+def _gpu(t):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("all tensors must live on the same GPU")
+    return dev
 
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+
+def _launch(name, dev, fn, *args):
+    """Calls a library function on `dev`'s current stream, with `dev` the current device
+    (the kernels run on that one)."""
+    if dev.index == _current_device():
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st != 0:
+        raise IdxError(name, st)
 
 
 def idx_page_tables(seq_len, n_new, table, free_ring, cursor, n_tokens, page_size=16,
@@ -434,10 +449,9 @@ def idx_page_tables(seq_len, n_new, table, free_ring, cursor, n_tokens, page_siz
     free_ring are updated in place. Returns PageTables; seq_len and cursor of the next
     step are its seq_len and cursor (n_tokens: rows of the packed new tokens;
     kv_indices: a buffer for the packed pages, as long as free_ring by default)."""
-    lib = load()
-    dev = _dev(seq_len, n_new, table, free_ring, cursor, kv_indices)
-    _int32(seq_len=seq_len, n_new=n_new, table=table, free_ring=free_ring, cursor=cursor,
-           kv_indices=kv_indices)
+    lib = _lib or load()
+    dev = _gpu(table)
+    _words(dev, table, seq_len, n_new, free_ring, cursor, kv_indices)
     B, max_pages = table.shape
     n_pages = free_ring.numel()
     if seq_len.numel() != B or n_new.numel() != B or cursor.numel() < 2:
@@ -445,110 +459,115 @@ def idx_page_tables(seq_len, n_new, table, free_ring, cursor, n_tokens, page_siz
     if n_tokens < 0:
         raise ValueError("n_tokens must not be negative")
     if kv_indices is None:
-        kv_indices = torch.empty(n_pages, dtype=torch.int32, device=dev)
-    # one allocation for the step's words, each list on a 16-byte border
-    up = lambda n: (n + 3) // 4 * 4  # noqa: E731
-    sizes = (B, 3, B + 1, B + 1, n_tokens, n_tokens, n_tokens)
-    buf = torch.empty(sum(up(n) for n in sizes), dtype=torch.int32, device=dev)
-    parts, at = [], 0
-    for n in sizes:
-        parts.append(buf[at:at + n])
-        at += up(n)
-    seq_out, cur_out, indptr, tok_indptr, slots, tok_req, tok_len = parts
-    with _on(dev):
-        _check("idx_page_tables", lib.idx_page_tables(
-            _ptr(seq_len), _ptr(n_new), _ptr(cursor), _ptr(table), _ptr(free_ring),
-            _ptr(seq_out), _ptr(cur_out), _ptr(indptr), _ptr(kv_indices), _ptr(tok_indptr),
-            _ptr(slots), _ptr(tok_req), _ptr(tok_len), B, max_pages, page_size, n_pages,
-            kv_indices.numel(), n_tokens, _stream(dev)))
+        kv_indices = torch.empty(n_pages, dtype=_I32, device=dev)
+    buf = torch.empty(3 * B + 5 + 3 * n_tokens, dtype=_I32, device=dev)
+    seq_out, cur_out, indptr, tok_indptr, slots, tok_req, tok_len = (
+        torch.unsafe_split_with_sizes(buf, (B, 3, B + 1, B + 1, n_tokens, n_tokens, n_tokens)))
+    at = buf.data_ptr()
+    rows = at + 4 * (3 * B + 5)
+    _launch("idx_page_tables", dev, lib.idx_page_tables, seq_len.data_ptr(), n_new.data_ptr(),
+            cursor.data_ptr(), table.data_ptr(), free_ring.data_ptr(), at, at + 4 * B,
+            at + 4 * (B + 3), kv_indices.data_ptr(), at + 4 * (2 * B + 4), rows,
+            rows + 4 * n_tokens, rows + 8 * n_tokens, B, max_pages, page_size, n_pages,
+            kv_indices.numel(), n_tokens)
     return PageTables(seq_out, cur_out, indptr, kv_indices, tok_indptr, slots, tok_req, tok_len)
 
 
 def _rows(name, x, dev):
     """A token-major tensor [n, heads, D] whose token rows may lie apart: its row
     stride in elements."""
-    if not x.is_cuda or x.device != dev:
+    if x.device != dev:
         raise ValueError("all tensors must live on the same GPU")
-    if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+    n, heads, D = x.shape
+    row, head, one = x.stride()
+    if one != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name} must be [tokens, heads, D] with dense heads")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return row if n > 1 else heads * D
 
 
-def _check_cache(k_cache, v_cache, k_scale, v_scale):
-    """Hkv, D, n_pages, page_size of a cache."""
-    for c in (k_cache, v_cache):
-        if c.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise TypeError("the caches must be float8_e4m3fn (or its codes as uint8)")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+def _cache(dev, k_cache, v_cache, k_scale, v_scale):
+    """Checks a cache; returns n_pages, Hkv, page_size, D."""
+    for t in (k_cache, v_cache, k_scale, v_scale):
+        if t.device != dev:
+            raise ValueError("all tensors must live on the same GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    if not (k_cache.dtype is v_cache.dtype is torch.float8_e4m3fn
+            or k_cache.dtype is v_cache.dtype is torch.uint8):
+        raise TypeError("the caches must be float8_e4m3fn (or its codes as uint8)")
+    if not k_scale.dtype is v_scale.dtype is torch.float32:
         raise TypeError("the scales must be float32")
-    n_pages, Hkv, page, D = k_cache.shape
-    if tuple(v_cache.shape) != (n_pages, Hkv, D, page):
+    n_pages, Hkv, page, D = shape = k_cache.shape
+    if v_cache.shape != (n_pages, Hkv, D, page):
         raise ValueError("v_cache must be [pages, Hkv, D, page_size] beside k_cache "
                          "[pages, Hkv, page_size, D]")
-    if tuple(k_scale.shape) != (n_pages, Hkv) or tuple(v_scale.shape) != (n_pages, Hkv):
+    if not k_scale.shape == v_scale.shape == (n_pages, Hkv):
         raise ValueError("the scales must be [pages, Hkv]")
-    return Hkv, D, n_pages, page
+    return shape
 
 
 def idx_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale):
     """Quantises the keys and values k, v [n, Hkv, 128] (float32 or bf16; token rows may
     lie apart) into their cache slots, one power-of-two scale per page and head. The
     tokens of one page lie in consecutive rows (as idx_page_tables orders them)."""
-    lib = load()
-    dev = _dev(k_cache, v_cache, k_scale, v_scale, slots)
-    Hkv, D, n_pages, page = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    lib = _lib or load()
+    dev = _gpu(k_cache)
+    n_pages, Hkv, page, D = _cache(dev, k_cache, v_cache, k_scale, v_scale)
     ks, vs = _rows("k", k, dev), _rows("v", v, dev)
-    _int32(slots=slots)
+    _words(dev, slots)
     n = slots.numel()
-    if tuple(k.shape) != (n, Hkv, D) or tuple(v.shape) != (n, Hkv, D) or k.dtype != v.dtype:
+    if not k.shape == v.shape == (n, Hkv, D) or k.dtype is not v.dtype:
         raise ValueError("k and v must be [slots, Hkv, D] of one dtype")
     if k.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"unsupported dtype {k.dtype}")
-    with _on(dev):
-        _check("idx_cache_write", lib.idx_cache_write(
-            _ptr(k), _ptr(v), ks, vs, _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), n, Hkv, D, n_pages, page, _dtype_code(k), _stream(dev)))
+    _launch("idx_cache_write", dev, lib.idx_cache_write, k.data_ptr(), v.data_ptr(), ks, vs,
+            slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), n, Hkv, D, n_pages, page, _dtype_code(k))
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K=0, page_size=16) -> int:
     return load().idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K, page_size)
 
 
+@functools.lru_cache(maxsize=1024)
 def idx_attend_prefill_workspace_bytes(n_tok, B, Hq, Hkv, max_pages, page_size=16) -> int:
     return load().idx_attend_prefill_workspace_bytes(n_tok, B, Hq, Hkv, max_pages, page_size)
 
 
-def _attend_inputs(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes,
-                   out, ws, scale, *more):
-    """Checks of both attention calls: (device, shapes, q's row stride, out, scale)."""
-    dev = _dev(k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes, out, ws,
-               *more)
-    shape = _check_cache(k_cache, v_cache, k_scale, v_scale)
+def _attend_inputs(dev, q, kv_len, slopes, out, ws):
+    """Checks what both attention calls take beside the cache: q's row stride, out."""
     stride = _rows("q", q, dev)
-    if q.dtype != torch.bfloat16:
-        raise TypeError("q must be bfloat16")
-    _int32(kv_indptr=kv_indptr, kv_indices=kv_indices, kv_len=kv_len)
     n, Hq, D = q.shape
-    if D != shape[1]:
-        raise ValueError("q and the cache differ in head dimension")
+    if q.dtype is not torch.bfloat16:
+        raise TypeError("q must be bfloat16")
     if kv_len.numel() != n:
         raise ValueError("kv_len must hold one entry per row of q")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != Hq):
-        raise ValueError("slopes must be float32, one per query head")
+    if slopes is not None:
+        if slopes.dtype is not torch.float32 or slopes.numel() != Hq or slopes.device != dev \
+                or not slopes.is_contiguous():
+            raise ValueError("slopes must be float32 on q's GPU, one per query head")
     if out is None:
         out = torch.empty(n, Hq, D, dtype=torch.bfloat16, device=dev)
-    elif out.dtype != torch.bfloat16 or out.shape != q.shape:
-        raise ValueError("out must be bfloat16 and shaped as q")
-    return dev, shape, stride, out, (D ** -0.5 if scale is None else scale)
+    elif (out.dtype is not torch.bfloat16 or out.shape != q.shape or out.device != dev
+          or not out.is_contiguous()):
+        raise ValueError("out must be contiguous bfloat16 on q's GPU, shaped as q")
+    if ws is not None and (ws.device != dev or ws.dtype is not torch.uint8
+                           or not ws.is_contiguous()):
+        raise ValueError("ws must be contiguous uint8 on q's GPU")
+    return stride, out
 
 
 def _scratch(nbytes, ws, dev):
-    """The workspace of an attention call: plain scratch, so it comes from torch's
-    allocator call by call (in stream order; inside a capture from the graph's own
-    memory) unless the caller brings one."""
-    if ws is not None or nbytes == 0:
-        return ws
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    """Pointer and size of an attention call's workspace (and the tensor, to be kept for
+    the call). It is plain scratch, so it comes from torch's allocator call by call (in
+    stream order; inside a capture from the graph's own memory) unless the caller brings
+    one."""
+    if ws is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages,
@@ -559,28 +578,29 @@ def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_
     idx_select_paged returns them. softcap: scores become softcap * tanh(x / softcap);
     slopes [Hq]: minus slope * distance. Returns out [R, Hq, 128]; a row that sees
     nothing is zero."""
-    lib = load()
-    dev, (Hkv, D, n_pages, page), stride, out, scale = _attend_inputs(
-        q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes, out, ws,
-        scale, row_req, ids)
-    _int32(row_req=row_req, ids=ids)
-    R, Hq, _ = q.shape
-    B = kv_indptr.numel() - 1
+    lib = _lib or load()
+    dev = _gpu(q)
+    n_pages, Hkv, page, D = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    _words(dev, kv_indptr, kv_indices, kv_len, row_req, ids)
+    stride, out = _attend_inputs(dev, q, kv_len, slopes, out, ws)
+    R, Hq, Dq = q.shape
+    if D != Dq:
+        raise ValueError("q and the cache differ in head dimension")
     if row_req is not None and row_req.numel() != R:
         raise ValueError("row_req must hold one entry per row of q")
-    if ids is not None and (ids.dim() != 2 or ids.shape[0] != R):
-        raise ValueError("ids must be [rows, K]")
-    K = 0 if ids is None else ids.shape[1]
-    if ids is not None and K == 0:
-        return out.zero_()
-    ws = _scratch(lib.idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K, page), ws, dev)
-    with _on(dev):
-        _check("idx_attend", lib.idx_attend(
-            _ptr(q), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_len), _ptr(row_req), _ptr(ids),
-            _ptr(slopes), _ptr(out), R, B, Hq, Hkv, D, n_pages, kv_indices.numel(), max_pages,
-            page, K, scale, softcap, IDX_BF16, _ptr(ws), 0 if ws is None else ws.numel(),
-            _stream(dev)))
+    K = 0
+    if ids is not None:
+        if ids.dim() != 2 or ids.shape[0] != R:
+            raise ValueError("ids must be [rows, K]")
+        K = ids.shape[1]
+        if K == 0:
+            return out.zero_()
+    wp, wn, ws = _scratch(idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K, page), ws, dev)
+    _launch("idx_attend", dev, lib.idx_attend, q.data_ptr(), stride, k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kv_indptr.data_ptr(),
+            kv_indices.data_ptr(), kv_len.data_ptr(), _ptr(row_req), _ptr(ids), _ptr(slopes),
+            out.data_ptr(), R, kv_indptr.numel() - 1, Hq, Hkv, D, n_pages, kv_indices.numel(),
+            max_pages, page, K, D ** -0.5 if scale is None else scale, softcap, IDX_BF16, wp, wn)
     return out
 
 
@@ -590,22 +610,25 @@ def idx_attend_prefill(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indi
     """idx_attend for packed prompt tokens q [n, Hq, 128]: request b's rows are
     tok_indptr[b]:tok_indptr[b+1], row t sees the first kv_len[t] tokens of its request
     (PageTables.tok_len: the causal mask). Rows of no request keep their output."""
-    lib = load()
-    dev, (Hkv, D, n_pages, page), stride, out, scale = _attend_inputs(
-        q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, slopes, out, ws,
-        scale, tok_indptr)
-    _int32(tok_indptr=tok_indptr)
-    n, Hq, _ = q.shape
+    lib = _lib or load()
+    dev = _gpu(q)
+    n_pages, Hkv, page, D = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    _words(dev, kv_indptr, kv_indices, tok_indptr, kv_len)
+    stride, out = _attend_inputs(dev, q, kv_len, slopes, out, ws)
+    n, Hq, Dq = q.shape
     B = kv_indptr.numel() - 1
+    if D != Dq:
+        raise ValueError("q and the cache differ in head dimension")
     if tok_indptr.numel() != B + 1:
         raise ValueError("tok_indptr and kv_indptr must both hold B + 1 entries")
-    ws = _scratch(lib.idx_attend_prefill_workspace_bytes(n, B, Hq, Hkv, max_pages, page), ws, dev)
-    with _on(dev):
-        _check("idx_attend_prefill", lib.idx_attend_prefill(
-            _ptr(q), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(kv_indptr), _ptr(kv_indices), _ptr(tok_indptr), _ptr(kv_len), _ptr(slopes),
-            _ptr(out), n, B, Hq, Hkv, D, n_pages, kv_indices.numel(), max_pages, page, scale,
-            softcap, IDX_BF16, _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    wp, wn, ws = _scratch(idx_attend_prefill_workspace_bytes(n, B, Hq, Hkv, max_pages, page), ws,
+                          dev)
+    _launch("idx_attend_prefill", dev, lib.idx_attend_prefill, q.data_ptr(), stride,
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            kv_indptr.data_ptr(), kv_indices.data_ptr(), tok_indptr.data_ptr(),
+            kv_len.data_ptr(), _ptr(slopes), out.data_ptr(), n, B, Hq, Hkv, D, n_pages,
+            kv_indices.numel(), max_pages, page, D ** -0.5 if scale is None else scale, softcap,
+            IDX_BF16, wp, wn)
     return out
 
 
