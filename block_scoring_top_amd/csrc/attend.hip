@@ -1,7 +1,8 @@
 // Attention of single tokens over the paged 8-bit cache (include/idx_cache.h,
 // idx_attend), and the join of partial results. The tile is in attend.hpp.
 //
-// One token's query heads of one KV head are the 16 (32, 64) rows of the products.
+// One token's query heads of one KV head are the 16 or 32 rows of the products (above 32
+// heads a group, two workgroups take 32 each).
 // Bound by reading the cache, 256 bytes a token and KV head: each of a workgroup's four
 // waves runs its own tiles, with its own softmax, joined in LDS at the end. Long rows are
 // cut into chunks of tiles for several workgroups; their partial sums are joined by
@@ -42,14 +43,15 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, int kblk, int ksub,
 }
 
 template <int NT, bool EXTRA>
-__global__ __launch_bounds__(kAtNT) void attend_rows_kernel(AttnArgs a, int chunk, int splits) {
+__global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int chunk, int splits,
+                                                               int bands) {
   __shared__ int u_blk[kChunkUnits], u_pos[kChunkUnits];
-  __shared__ float u_ks[kChunkUnits], u_vs[kChunkUnits];
   __shared__ float s_m[kAtWaves][16 * NT], s_l[kAtWaves][16 * NT];
   __shared__ __attribute__((aligned(16))) float s_o[16 * NT][kRowPad];
 
-  const int h = blockIdx.x % a.Hkv;
-  const int rest = blockIdx.x / a.Hkv;
+  const int band = blockIdx.x % bands;  // of 16 NT query heads of the group
+  const int h = blockIdx.x / bands % a.Hkv;
+  const int rest = blockIdx.x / bands / a.Hkv;
   const int split = rest % splits, r = rest / splits;
   const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
   const int n = lane & 15, g = lane >> 4;
@@ -81,8 +83,6 @@ __global__ __launch_bounds__(kAtNT) void attend_rows_kernel(AttnArgs a, int chun
     }
     u_blk[i] = blk;
     u_pos[i] = blk < 0 ? 0 : pos;
-    u_ks[i] = blk < 0 ? 0.f : a.k_scale[blk] * a.score_scale;
-    u_vs[i] = blk < 0 ? 0.f : a.v_scale[blk];
   }
 
   at_bf16x8 q[NT][4];
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kAtNT) void attend_rows_kernel(AttnArgs a, int chun
   int len[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int hq = h * G + min(16 * j + n, G - 1);
+    const int hq = h * G + min(16 * NT * band + 16 * j + n, G - 1);
     load_query(a.q + (int64_t)r * a.q_stride + hq * kHeadDim, g, q[j]);
     slope2[j] = EXTRA ? slope_of(a, hq) : 0.f;
     len[j] = seen;
@@ -104,16 +104,19 @@ __global__ __launch_bounds__(kAtNT) void attend_rows_kernel(AttnArgs a, int chun
     const int kblk = u_blk[ku], vblk = u_blk[vu], pos = u_pos[vu];
     const int have = vblk < 0 ? 0 : min(seen - pos, kUnit);
     if (__all(have == 0)) continue;
+    // (its scales are asked for with the codes, not while the units are listed: a
+    // workgroup's start is a chain of loads already)
     uint4 k[4][2], v[8];
-    load_tile(a, kblk, (u_pos[ku] % a.page_size) / kUnit, vblk, (pos % a.page_size) / kUnit, n,
-              g, k, v);
+    const float ks = a.k_scale[max(vblk, 0)], vs = a.v_scale[max(vblk, 0)];
+    load_tile(a, kblk, (u_pos[ku] & (a.page_size - 1)) / kUnit, vblk,
+              (pos & (a.page_size - 1)) / kUnit, n, g, k, v);
     const bool any = !__all(have == kUnit);
     if (any) {
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
     }
-    attn_tile<NT, EXTRA>(st, q, k, v, u_ks[vu], u_vs[vu], pos, have, len, slope2, a.softcap,
-                         any);
+    attn_tile<NT, EXTRA>(st, q, k, v, vblk < 0 ? 0.f : ks * a.score_scale,
+                         vblk < 0 ? 0.f : vs, pos, have, len, slope2, a.softcap, any);
   }
 
   // join the waves
@@ -148,8 +151,9 @@ __global__ __launch_bounds__(kAtNT) void attend_rows_kernel(AttnArgs a, int chun
     __syncthreads();
   }
   const int64_t part = ((int64_t)r * a.Hkv + h) * splits + split;
-  for (int item = tid; item < G * 16; item += kAtNT) {
-    const int row = item >> 4, d = (item & 15) * 8;
+  const int rows = min(16 * NT, G - 16 * NT * band);
+  for (int item = tid; item < rows * 16; item += kAtNT) {
+    const int row = item >> 4, d = (item & 15) * 8, g_row = 16 * NT * band + row;
     float m = s_m[0][row], l = 0.f;
 #pragma unroll
     for (int i = 1; i < kAtWaves; ++i) m = fmaxf(m, s_m[i][row]);
@@ -164,58 +168,106 @@ __global__ __launch_bounds__(kAtNT) void attend_rows_kernel(AttnArgs a, int chun
       out.y = pack_bf16(o[2] * inv, o[3] * inv);
       out.z = pack_bf16(o[4] * inv, o[5] * inv);
       out.w = pack_bf16(o[6] * inv, o[7] * inv);
-      *reinterpret_cast<uint4*>(a.out + ((int64_t)r * a.Hq + h * G + row) * kHeadDim + d) = out;
+      *reinterpret_cast<uint4*>(a.out + ((int64_t)r * a.Hq + h * G + g_row) * kHeadDim + d) = out;
     } else {
-      at_f32x4* p = reinterpret_cast<at_f32x4*>(a.part_o + (part * G + row) * kHeadDim + d);
+      at_f32x4* p = reinterpret_cast<at_f32x4*>(a.part_o + (part * G + g_row) * kHeadDim + d);
       p[0] = *reinterpret_cast<const at_f32x4*>(o);
       p[1] = *reinterpret_cast<const at_f32x4*>(o + 4);
       if (d == 0) {
-        a.part_ml[2 * (part * G + row)] = m;
-        a.part_ml[2 * (part * G + row) + 1] = l;
+        a.part_ml[2 * (part * G + g_row)] = m;
+        a.part_ml[2 * (part * G + g_row) + 1] = l;
       }
     }
   }
 }
 
-// One wave per (row, query head): the splits' sums, each in units of its own maximum.
-__global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t rows,
+// The splits' sums of one (row, query head), each in units of its own maximum: TEAMS
+// teams of 32 lanes, four dims a lane, take every TEAMS-th split, four at a time with
+// their loads in flight, and are joined in LDS. Fixed orders: the same sums every time.
+template <int TEAMS>
+__global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t items,
                                                              int splits) {
-  const int64_t item = (int64_t)blockIdx.x * kAtWaves + threadIdx.x / kWave;
-  if (item >= rows * a.Hq) return;
-  const int lane = lane_id();
+  constexpr int kItems = kAtNT / 32 / TEAMS;  // of a workgroup
+  __shared__ __attribute__((aligned(16))) float s_o[kAtNT / 32][kHeadDim];
+  __shared__ float s_m[kAtNT / 32], s_l[kAtNT / 32];
+  const int lane = threadIdx.x & 31, group = threadIdx.x / 32, team = group % TEAMS;
+  const int64_t item = (int64_t)blockIdx.x * kItems + group / TEAMS;
   const int G = a.Hq / a.Hkv;
   const int64_t r = item / a.Hq;
+  const int hq = (int)(item % a.Hq), h = hq / G;
   // prompt rows of no request keep their output
-  if (a.tok_indptr != nullptr && (r < a.tok_indptr[0] || r >= a.tok_indptr[a.B])) return;
-  const int hq = (int)(item % a.Hq), h = hq / G, row = hq % G;
-  const int64_t first = ((r * a.Hkv + h) * splits) * G + row;  // + s * G
-  float m = -__builtin_inff();
-  for (int s = lane; s < splits; s += kWave) m = fmaxf(m, a.part_ml[2 * (first + (int64_t)s * G)]);
+  const bool live = item < items && (a.tok_indptr == nullptr ||
+                                     (r >= a.tok_indptr[0] && r < a.tok_indptr[a.B]));
+  const int64_t first = ((r * a.Hkv + h) * splits) * G + hq % G;  // + s * G
+  float m = -__builtin_inff(), l = 0.f;
+  at_f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  if (live) {
+    constexpr int kStep = 4;
+    for (int s0 = team; s0 < splits; s0 += kStep * TEAMS) {
+      at_f32x2 ml[kStep];
+      at_f32x4 x[kStep];
 #pragma unroll
-  for (int d = 1; d < kWave; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-  const float base = m == -__builtin_inff() ? 0.f : m;
-  float l = 0.f;
-  at_f32x2 o = {0.f, 0.f};
-  for (int s = 0; s < splits; ++s) {
-    const int64_t p = first + (int64_t)s * G;
-    const float ls = a.part_ml[2 * p + 1];
-    if (ls == 0.f) continue;
-    const float f = exp2_fast(a.part_ml[2 * p] - base);
-    l += ls * f;
-    o += *reinterpret_cast<const at_f32x2*>(a.part_o + p * kHeadDim + 2 * lane) * f;
+      for (int i = 0; i < kStep; ++i) {
+        const int s = s0 + i * TEAMS;
+        const int64_t p = first + (int64_t)min(s, splits - 1) * G;
+        ml[i] = *reinterpret_cast<const at_f32x2*>(a.part_ml + 2 * p);
+        x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
+        if (s >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) top = fmaxf(top, ml[i][0]);
+      const float base = top == -__builtin_inff() ? 0.f : top;
+      const float f = exp2_fast(m - base);
+      m = top;
+      l *= f;
+      o *= f;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        if (ml[i][1] == 0.f) continue;  // a split without tokens: its sums are not written
+        const float w = exp2_fast(ml[i][0] - base);
+        l += ml[i][1] * w;
+        o += x[i] * w;
+      }
+    }
+  }
+  *reinterpret_cast<at_f32x4*>(&s_o[group][4 * lane]) = o;
+  if (lane == 0) {
+    s_m[group] = m;
+    s_l[group] = l;
+  }
+  __syncthreads();
+  if (!live || team != 0) return;
+  float top = m;
+#pragma unroll
+  for (int i = 1; i < TEAMS; ++i) top = fmaxf(top, s_m[group + i]);
+  const float base = top == -__builtin_inff() ? 0.f : top;
+  const float f = exp2_fast(m - base);
+  l *= f;
+  o *= f;
+#pragma unroll
+  for (int i = 1; i < TEAMS; ++i) {
+    const float w = exp2_fast(s_m[group + i] - base);
+    l += s_l[group + i] * w;
+    o += *reinterpret_cast<const at_f32x4*>(&s_o[group + i][4 * lane]) * w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint32_t*>(a.out + (r * a.Hq + hq) * kHeadDim)[lane] =
-      pack_bf16(o[0] * inv, o[1] * inv);
+  reinterpret_cast<uint2*>(a.out + (r * a.Hq + hq) * kHeadDim)[lane] =
+      make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
 }
 
 }  // namespace
 
+// Rows are cut only when there are fewer than two workgroups a CU without it (the GQA
+// batch of 128 rows on 4 heads, 256 pages each: 102 us whole, 108 in two). Then into
+// chunks that would give eight a CU if all rows were of the longest length, so that
+// ragged rows still balance (4 rows of 4096 to 131072 tokens on 8 heads: 148 us at two a
+// CU, 136 at four, 123 at eight, 127 at sixteen), down to a tile for each wave.
 AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
   const int64_t tiles = (units + 3) / 4;
   const int64_t pairs = R * Hkv;
-  int64_t splits = (1024 + pairs - 1) / pairs;            // about four workgroups a CU
-  splits = splits < tiles / 8 ? splits : tiles / 8;       // at least two tiles a wave
+  int64_t splits = pairs >= 512 ? 1 : (2048 + pairs - 1) / pairs;
+  if (splits > tiles / kAtWaves) splits = tiles / kAtWaves;
   if (splits < 1) splits = 1;
   int64_t chunk = (tiles + splits - 1) / splits;
   if (chunk > kChunkTiles) chunk = kChunkTiles;
@@ -223,10 +275,17 @@ AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
 }
 
 int launch_attend_merge(const AttnArgs& a, int splits, void* stream) {
-  const int64_t rows = a.R;
-  const int64_t grid = (rows * a.Hq + kAtWaves - 1) / kAtWaves;
-  hipLaunchKernelGGL(attend_merge_kernel, dim3((unsigned)grid), dim3(kAtNT), 0,
-                     static_cast<hipStream_t>(stream), a, rows, splits);
+  const int64_t items = (int64_t)a.R * a.Hq;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  // few items of many splits: a workgroup for each (128 items of 32 splits: 18 us with a
+  // wave for each and one split at a time, 4.8 so)
+  const bool wide = splits > 8 && items <= 8192;
+  const int per = wide ? 1 : 4;
+  const dim3 grid((unsigned)((items + per - 1) / per)), blk(kAtNT);
+  if (wide)
+    hipLaunchKernelGGL((attend_merge_kernel<8>), grid, blk, 0, s, a, items, splits);
+  else
+    hipLaunchKernelGGL((attend_merge_kernel<2>), grid, blk, 0, s, a, items, splits);
   return (int)hipGetLastError();
 }
 
@@ -234,15 +293,15 @@ int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int G = a.Hq / a.Hkv;
   const bool extra = a.softcap > 0.f || a.slopes != nullptr;
-  const dim3 grid((unsigned)((int64_t)a.R * a.Hkv * sp.splits)), blk(kAtNT);
-#define IDX_ROWS(NT, EX) \
-  hipLaunchKernelGGL((attend_rows_kernel<NT, EX>), grid, blk, 0, s, a, sp.chunk, sp.splits)
+  const int bands = G <= 32 ? 1 : 2;
+  const dim3 grid((unsigned)((int64_t)a.R * a.Hkv * sp.splits * bands)), blk(kAtNT);
+#define IDX_ROWS(NT, EX)                                                                      \
+  hipLaunchKernelGGL((attend_rows_kernel<NT, EX>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
+                     bands)
   if (G <= 16) {
     if (extra) IDX_ROWS(1, true); else IDX_ROWS(1, false);
-  } else if (G <= 32) {
-    if (extra) IDX_ROWS(2, true); else IDX_ROWS(2, false);
   } else {
-    if (extra) IDX_ROWS(4, true); else IDX_ROWS(4, false);
+    if (extra) IDX_ROWS(2, true); else IDX_ROWS(2, false);
   }
 #undef IDX_ROWS
   int e = (int)hipGetLastError();
