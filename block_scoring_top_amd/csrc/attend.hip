@@ -85,13 +85,14 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
     u_pos[i] = blk < 0 ? 0 : pos;
   }
 
+  const float call_scale = fabsf(a.score_scale);
   at_bf16x8 q[NT][4];
   float slope2[NT];
   int len[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int hq = h * G + min(16 * NT * band + 16 * j + n, G - 1);
-    load_query(a.q + (int64_t)r * a.q_stride + hq * kHeadDim, g, q[j]);
+    load_query(a.q + (int64_t)r * a.q_stride + hq * kHeadDim, g, a.score_scale < 0.f, q[j]);
     slope2[j] = EXTRA ? slope_of(a, hq) : 0.f;
     len[j] = seen;
   }
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
     }
-    attn_tile<NT, EXTRA>(st, q, k, v, vblk < 0 ? 0.f : ks * a.score_scale,
+    attn_tile<NT, EXTRA>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
                          vblk < 0 ? 0.f : vs, pos, have, len, slope2, a.softcap, any);
   }
 

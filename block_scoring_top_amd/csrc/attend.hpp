@@ -11,8 +11,11 @@
 //     those tokens at one dim, is 8 consecutive bytes of the value cache;
 // so neither scores nor values cross lanes, and both caches go straight from memory
 // into registers, 16 bytes a lane.
-// A probability is held as 2^(x - m + kPBias): fp16 then keeps 11 bits of every
-// probability down to 2^-28 of the row's largest.
+// A probability is held as 2^(x - m + kPBias), with a reference m that is moved only when
+// the row's maximum has grown by kLazy or more (most tiles then leave the sums alone): it
+// reaches 2^(kPBias + kLazy), which fp16 holds, and keeps 11 bits down to 2^-23 of the
+// row's largest. The value scale of a unit enters with the exponential's argument, as a
+// logarithm relative to the largest scale met, and leaves the sum of weights once a unit.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -32,7 +35,8 @@ typedef float at_f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 16;       // tokens of a unit
 constexpr int kTileTok = 64;    // tokens of a tile: one unit per lane group
-constexpr float kPBias = 14.f;  // probabilities reach 2^14
+constexpr float kPBias = 9.f;
+constexpr float kLazy = 6.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // four e4m3 codes -> bf16 / fp16 (both exact)
@@ -84,17 +88,14 @@ __device__ __forceinline__ float capped(float x, float cap) {
   return cap * kLog2e * __builtin_fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + e), 1.f);
 }
 
-// The score of one token in base-2 units. ksc holds the page's key scale, the call's
-// scale and, for uncapped scores, log2(e); dist = visible length - 1 - position.
-template <bool EXTRA>
+// The capped or biased score of one token in base-2 units. ksc holds the page's key
+// scale, the call's scale and, for uncapped scores, log2(e); dist = visible length - 1 -
+// position.
 __device__ __forceinline__ float score2(float dot, float ksc, float softcap, float slope2,
                                         float dist) {
   float x = dot * ksc;
-  if constexpr (EXTRA) {
-    if (softcap > 0.f) x = capped(x, softcap);
-    x -= slope2 * dist;
-  }
-  return x;
+  if (softcap > 0.f) x = capped(x, softcap);
+  return x - slope2 * dist;
 }
 
 // the running softmax of NT tiles of 16 query rows
@@ -102,12 +103,13 @@ template <int NT>
 struct AttnState {
   at_f32x4 o[NT][8];  // dims 16 dt + 4 g + i of query row n
   float m[NT], l[NT];  // m: all groups alike; l: this group's units alone
-  float vref;          // largest value scale met: o is in its units
+  float vref, lref;    // largest value scale met, and its logarithm: o is in its units
 };
 
 template <int NT>
 __device__ __forceinline__ void attn_init(AttnState<NT>& st) {
   st.vref = 0.f;
+  st.lref = 0.f;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     st.m[j] = -__builtin_inff();
@@ -118,14 +120,19 @@ __device__ __forceinline__ void attn_init(AttnState<NT>& st) {
 }
 
 // Query rows of a lane as the B operand: chunk (c, half) holds dims
-// 64 c + 16 g + 8 half .. + 7 of query row n.
-__device__ __forceinline__ void load_query(const uint16_t* row, int g, at_bf16x8 (&q)[4]) {
+// 64 c + 16 g + 8 half .. + 7 of query row n. A negative call scale turns the queries'
+// signs, so that scores keep their order under the (positive) scale of a unit.
+__device__ __forceinline__ void load_query(const uint16_t* row, int g, bool negative,
+                                           at_bf16x8 (&q)[4]) {
+  const uint32_t sign = negative ? 0x80008000u : 0u;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int half = 0; half < 2; ++half) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + 64 * c + 16 * g + 8 * half);
       q[2 * c + half] = __builtin_bit_cast(
-          at_bf16x8, *reinterpret_cast<const uint4*>(row + 64 * c + 16 * g + 8 * half));
+          at_bf16x8, make_uint4(x.x ^ sign, x.y ^ sign, x.z ^ sign, x.w ^ sign));
+    }
 }
 
 // One tile. k: this lane's key bytes, k[s][c] = dims 64 c + 16 g .. + 15 of token
@@ -139,18 +146,19 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
                                           const uint4 (&k)[4][2], const uint4 (&v)[8], float ksc,
                                           float vs, int pos, int have, const int (&len)[NT],
                                           const float (&slope2)[NT], float softcap, bool any) {
-  // Values enter the product as bare codes; their scales go into the probabilities,
-  // relative to the largest one met, so that fp16 holds them.
   const float vtop = groups_max(vs);
   if (vtop > st.vref) {
     const float f = st.vref / vtop;
     st.vref = vtop;
+    st.lref = __log2f(vtop);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) st.o[j][dt] *= f;
   }
-  const float vsc = vs == st.vref ? 1.f : vs / st.vref;
+  // (below 2^-60 of the largest, fp16 holds nothing of it)
+  const float lv = vs == st.vref ? 0.f : fmaxf(__log2f(vs) - st.lref, -60.f);
+  const float unlv = exp2_fast(-lv);
   at_f32x4 x[NT][4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -176,35 +184,41 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = 4 * s + i;
-        float y = score2<EXTRA>(x[j][s][i], ksc, softcap, slope2[j],
-                                EXTRA ? (float)(len[j] - 1 - pos - tok) : 0.f);
+        float y = x[j][s][i];
+        if constexpr (EXTRA)
+          y = score2(y, ksc, softcap, slope2[j], (float)(len[j] - 1 - pos - tok));
         if (any) y = (tok < have && pos + tok < len[j]) ? y : -__builtin_inff();
         x[j][s][i] = y;
         top = fmaxf(top, y);
       }
-    const float m = fmaxf(st.m[j], groups_max(top));
-    const float base = (m == -__builtin_inff() ? 0.f : m);
-    const float alpha = exp2_fast(st.m[j] - base);
-    st.m[j] = m;
-    float sum = 0.f;
+    // uncapped scores are scaled by ksc > 0 from here on (not 0, for masked ones)
+    const float sc = EXTRA ? 1.f : fmaxf(ksc, 1e-30f);
+    top = groups_max(top * sc);
+    if (__any(top > st.m[j] + kLazy)) {
+      const float m = fmaxf(st.m[j], top);
+      const float f = exp2_fast(st.m[j] - (m == -__builtin_inff() ? 0.f : m));
+      st.m[j] = m;
+      st.l[j] *= f;
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt) st.o[j][dt] *= f;
+    }
+    const float off = (st.m[j] == -__builtin_inff() ? 0.f : st.m[j]) - kPBias - lv;
+    float sum[2] = {0.f, 0.f};
     uint32_t w[8];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       float e[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        e[i] = exp2_fast(x[j][s][i] - (base - kPBias));
-        sum += e[i];
-        e[i] *= vsc;
+        e[i] = exp2_fast(__builtin_fmaf(x[j][s][i], sc, -off));
+        sum[i & 1] += e[i];
       }
       w[2 * s] = pack_f16(e[0], e[1]);
       w[2 * s + 1] = pack_f16(e[2], e[3]);
     }
     p[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
     p[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
-    st.l[j] = st.l[j] * alpha + sum;
-#pragma unroll
-    for (int dt = 0; dt < 8; ++dt) st.o[j][dt] *= alpha;
+    st.l[j] = __builtin_fmaf(sum[0] + sum[1], unlv, st.l[j]);
   }
 #pragma unroll
   for (int dt = 0; dt < 8; ++dt) {

@@ -18,7 +18,7 @@
 //     value scale back out, once a unit.
 //   - The reference of a row is moved only when its maximum has grown by 2^kLazy or
 //     more (sums are rescaled then); until that, probabilities reach up to 2^kLazy
-//     times 2^kPreBias, which fp16 holds.
+//     times 2^kPBias, which fp16 holds.
 // Two prompts of 8009 and 8192 tokens, 32 heads on 8: 1.15 ms, 0.93 PFLOP/s (a large
 // library product reaches 1.21 on this card); 3.76 ms with 16 rows a product straight from
 // the cache. Bound by the products and the exponentials beside them at the clock the card
@@ -42,8 +42,6 @@ constexpr int kPreNT = kPreWaves * kWave;
 constexpr int kPreRows = 32 * kPreWaves;
 constexpr int kPreChunk = 512;                // most tiles of a workgroup: page data in LDS
 constexpr int kPreUnits = 4 * (kPreChunk + 4);  // and for the tiles loaded ahead
-constexpr float kPreBias = 9.f;
-constexpr float kLazy = 6.f;
 // what happens to a score beside its scale; capped ones may be biased too
 constexpr int kPlain = 0, kBiased = 1, kCapped = 2;
 constexpr int kAhead = 4;                     // operands read from LDS before their use
@@ -324,7 +322,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     uint4 p[4];
 #pragma unroll
     for (int ts = 0; ts < 2; ++ts) {
-      const float off = base - kPreBias - lv[ts];
+      const float off = base - kPBias - lv[ts];
       float sum = 0.f;
       uint32_t wd[8];
 #pragma unroll
