@@ -42,7 +42,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, int kblk, int ksub,
     v[dt] = *reinterpret_cast<const uint4*>(vp + (int64_t)dt * 16 * a.page_size);
 }
 
-template <int NT, bool EXTRA>
+template <int NT, int KIND>
 __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int chunk, int splits,
                                                                int bands) {
   __shared__ int u_blk[kChunkUnits], u_pos[kChunkUnits];
@@ -86,6 +86,7 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   }
 
   const float call_scale = fabsf(a.score_scale);
+  const Cap cap(a.softcap);
   at_bf16x8 q[NT][4];
   float slope2[NT];
   int len[NT];
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   for (int j = 0; j < NT; ++j) {
     const int hq = h * G + min(16 * NT * band + 16 * j + n, G - 1);
     load_query(a.q + (int64_t)r * a.q_stride + hq * kHeadDim, g, a.score_scale < 0.f, q[j]);
-    slope2[j] = EXTRA ? slope_of(a, hq) : 0.f;
+    slope2[j] = KIND != kPlain ? slope_of(a, hq) : 0.f;
     len[j] = seen;
   }
   AttnState<NT> st;
@@ -116,8 +117,8 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
     }
-    attn_tile<NT, EXTRA>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
-                         vblk < 0 ? 0.f : vs, pos, have, len, slope2, a.softcap, any);
+    attn_tile<NT, KIND>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
+                         vblk < 0 ? 0.f : vs, pos, have, len, slope2, cap, any);
   }
 
   // join the waves
@@ -293,17 +294,21 @@ int launch_attend_merge(const AttnArgs& a, int splits, void* stream) {
 int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int G = a.Hq / a.Hkv;
-  const bool extra = a.softcap > 0.f || a.slopes != nullptr;
   const int bands = G <= 32 ? 1 : 2;
   const dim3 grid((unsigned)((int64_t)a.R * a.Hkv * sp.splits * bands)), blk(kAtNT);
-#define IDX_ROWS(NT, EX)                                                                      \
-  hipLaunchKernelGGL((attend_rows_kernel<NT, EX>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
+#define IDX_ROWS(NT, KIND)                                                                      \
+  hipLaunchKernelGGL((attend_rows_kernel<NT, KIND>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
                      bands)
+#define IDX_KINDS(NT)                                \
+  if (a.softcap > 0.f) IDX_ROWS(NT, kCapped);        \
+  else if (a.slopes != nullptr) IDX_ROWS(NT, kBiased); \
+  else IDX_ROWS(NT, kPlain)
   if (G <= 16) {
-    if (extra) IDX_ROWS(1, true); else IDX_ROWS(1, false);
+    IDX_KINDS(1);
   } else {
-    if (extra) IDX_ROWS(2, true); else IDX_ROWS(2, false);
+    IDX_KINDS(2);
   }
+#undef IDX_KINDS
 #undef IDX_ROWS
   int e = (int)hipGetLastError();
   if (e == 0 && sp.splits > 1) e = launch_attend_merge(a, sp.splits, stream);

@@ -81,21 +81,26 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v + __uint_as_float(lane_xor<32>(__float_as_uint(v)));
 }
 
-// cap * tanh(x / cap) in base-2 units, by tanh y = 1 - 2 / (1 + e^(2y)): y large gives
-// 1, y small -1, no overflow
-__device__ __forceinline__ float capped(float x, float cap) {
-  const float e = exp2_fast(x * (2.f * kLog2e / cap));
-  return cap * kLog2e * __builtin_fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + e), 1.f);
-}
+// What happens to a score beside its scale (a capped one may be biased too).
+constexpr int kPlain = 0, kBiased = 1, kCapped = 2;
 
-// The capped or biased score of one token in base-2 units. ksc holds the page's key
-// scale, the call's scale and, for uncapped scores, log2(e); dist = visible length - 1 -
-// position.
-__device__ __forceinline__ float score2(float dot, float ksc, float softcap, float slope2,
-                                        float dist) {
-  float x = dot * ksc;
-  if (softcap > 0.f) x = capped(x, softcap);
-  return x - slope2 * dist;
+// The constants of capped scores, cap * tanh(x / cap) in base-2 units, by
+// tanh y = 1 - 2 / (1 + e^(2y)): y large gives 1, y small -1, no overflow.
+struct Cap {
+  float in, out;  // exponent of a unit-scaled product; cap in base-2 units
+  __device__ __forceinline__ explicit Cap(float cap)
+      : in(cap > 0.f ? 2.f * kLog2e / cap : 0.f), out(cap * kLog2e) {}
+};
+
+// The capped or biased score of a token: ksc holds the page's key scale, the call's
+// scale and, for uncapped scores, log2(e); bias = -slope * distance.
+template <int KIND>
+__device__ __forceinline__ float score2(float dot, float ksc, const Cap& cap, float bias) {
+  if constexpr (KIND == kCapped) {
+    const float r = __builtin_amdgcn_rcpf(1.f + exp2_fast(dot * (ksc * cap.in)));
+    return __builtin_fmaf(-2.f * cap.out, r, cap.out) + bias;
+  }
+  return __builtin_fmaf(dot, ksc, bias);
 }
 
 // the running softmax of NT tiles of 16 query rows
@@ -141,11 +146,11 @@ __device__ __forceinline__ void load_query(const uint16_t* row, int g, bool nega
 // position of its first token; have: how many of its tokens exist; len: visible length
 // of each of the lane's query rows; any: whether a token of the tile is masked for any
 // row (uniform over the wave).
-template <int NT, bool EXTRA>
+template <int NT, int KIND>
 __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q)[NT][4],
                                           const uint4 (&k)[4][2], const uint4 (&v)[8], float ksc,
                                           float vs, int pos, int have, const int (&len)[NT],
-                                          const float (&slope2)[NT], float softcap, bool any) {
+                                          const float (&slope2)[NT], const Cap& cap, bool any) {
   const float vtop = groups_max(vs);
   if (vtop > st.vref) {
     const float f = st.vref / vtop;
@@ -179,20 +184,21 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     float top = -__builtin_inff();
+    const float bias = KIND == kPlain ? 0.f : -slope2[j] * (float)(len[j] - 1 - pos);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = 4 * s + i;
         float y = x[j][s][i];
-        if constexpr (EXTRA)
-          y = score2(y, ksc, softcap, slope2[j], (float)(len[j] - 1 - pos - tok));
+        if constexpr (KIND != kPlain)
+          y = score2<KIND>(y, ksc, cap, __builtin_fmaf((float)tok, slope2[j], bias));
         if (any) y = (tok < have && pos + tok < len[j]) ? y : -__builtin_inff();
         x[j][s][i] = y;
         top = fmaxf(top, y);
       }
     // uncapped scores are scaled by ksc > 0 from here on (not 0, for masked ones)
-    const float sc = EXTRA ? 1.f : fmaxf(ksc, 1e-30f);
+    const float sc = KIND != kPlain ? 1.f : fmaxf(ksc, 1e-30f);
     top = groups_max(top * sc);
     if (__any(top > st.m[j] + kLazy)) {
       const float m = fmaxf(st.m[j], top);

@@ -42,8 +42,6 @@ constexpr int kPreNT = kPreWaves * kWave;
 constexpr int kPreRows = 32 * kPreWaves;
 constexpr int kPreChunk = 512;                // most tiles of a workgroup: page data in LDS
 constexpr int kPreUnits = 4 * (kPreChunk + 4);  // and for the tiles loaded ahead
-// what happens to a score beside its scale; capped ones may be biased too
-constexpr int kPlain = 0, kBiased = 1, kCapped = 2;
 constexpr int kAhead = 4;                     // operands read from LDS before their use
 constexpr int kFrag = kWave;                  // uint4s of one operand in LDS
 
@@ -122,6 +120,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     }
   }
   const float call_scale = fabsf(a.score_scale);
+  const Cap cap(a.softcap);
 
   int longest = len, shortest = row < rows ? len : 0x7FFFFFFF;  // of the wave's rows
 #pragma unroll
@@ -272,8 +271,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float c0 = __builtin_fmaf((float)j, slope2, bias);
-          x[ts][j] = KIND == kCapped ? capped(x[ts][j] * ksc[ts], a.softcap) + c0
-                                     : __builtin_fmaf(x[ts][j], ksc[ts], c0);
+          x[ts][j] = score2<KIND>(x[ts][j], ksc[ts], cap, c0);
         }
         ksc[ts] = 1.f;
       }
