@@ -75,8 +75,11 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   __shared__ PreLds lds;
   const int h = blockIdx.x % a.Hkv;
   const int rest = blockIdx.x / a.Hkv;
-  const int split = rest % splits;
-  const int64_t tile = n_tiles - 1 - rest / splits;  // a prompt's last tokens see most
+  // the row tiles of one stretch of keys side by side: they share it in L2, one KV head to
+  // an XCD where there are eight (or the heads divide them); a prompt's last tokens, which
+  // see most, first
+  const int split = (int)(rest / n_tiles);
+  const int64_t tile = n_tiles - 1 - rest % n_tiles;
   const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
   const int n = lane & 31, half = lane >> 5;
   const int G = a.Hq / a.Hkv;
@@ -412,11 +415,12 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 
 int64_t attend_prefill_tiles(int64_t n_tok, int B, int G) { return n_tok * G / kPreRows + B; }
 
-// A long context is cut so that about 512 workgroups share the call, but not below 32 tiles
-// each (a workgroup's start, and its partial sums, written and read again, cost about five
-// tiles' time: chunks of 512 tokens on 4608 and 30512, 32 heads on 8, took 486 us at 512
-// workgroups wanted, 513 at 1024, 520 at 1536); a call of few workgroups into as many as
-// there are CUs, down to four tiles (five tokens on 900 to 2777: 29 us before, 22 so).
+// A call of fewer than two workgroups a CU is cut along its keys into about 1536, but not
+// below 32 tiles each: a workgroup's start and end cost four tiles' time, and its partial
+// sums are written and read again (chunks of 512 tokens on 4608 and 30512, 32 heads on 8:
+// 492 us at 512 wanted, 484 at 1536; the two prompts of 8192, 2032 workgroups: 1.14 ms
+// whole, 1.42 in two). One of fewer workgroups than CUs goes down to four tiles (five
+// tokens on 900 to 2777: 29 us at eight, 22 so).
 AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
   const int64_t tiles = (units + 3) / 4;
   const int64_t groups = attend_prefill_tiles(n_tok, B, Hq / Hkv) * Hkv;
@@ -426,7 +430,7 @@ AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t un
   };
   int64_t splits = 1;
   if (most(256, 4) > splits) splits = most(256, 4);
-  if (most(512, 32) > splits) splits = most(512, 32);
+  if (groups < 512 && most(1536, 32) > splits) splits = most(1536, 32);
   int64_t chunk = (tiles + splits - 1) / splits;
   if (chunk > kPreChunk) chunk = kPreChunk;
   return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
