@@ -19,8 +19,8 @@ namespace {
 
 constexpr int kAtNT = 256;
 constexpr int kAtWaves = kAtNT / kWave;
-constexpr int kChunkTiles = 256;              // most tiles of one workgroup
-constexpr int kChunkUnits = 4 * kChunkTiles;
+constexpr int kPhase = 256;                   // tiles whose pages wait in LDS
+constexpr int kPhaseUnits = 4 * kPhase;
 constexpr int kRowPad = kHeadDim + 4;         // floats of a row of sums in LDS
 
 // Loads of one tile: this lane's key bytes (unit m / 4) and value bytes (unit g).
@@ -45,7 +45,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, int kblk, int ksub,
 template <int NT, int KIND>
 __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int chunk, int splits,
                                                                int bands) {
-  __shared__ int u_blk[kChunkUnits], u_pos[kChunkUnits];
+  __shared__ int u_blk[kPhaseUnits], u_pos[kPhaseUnits];
   __shared__ float s_m[kAtWaves][16 * NT], s_l[kAtWaves][16 * NT];
   __shared__ __attribute__((aligned(16))) float s_o[16 * NT][kRowPad];
 
@@ -63,28 +63,6 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   const PageList pages = known ? page_list(a, b) : PageList{0, 0};
   const int seen = known ? max(a.kv_len[r], 0) : 0;
 
-  // this workgroup's units: list slots or selected slots, 16 tokens each
-  const int64_t listed =
-      a.ids != nullptr ? (int64_t)a.K * upp
-                       : min((int64_t)pages.n * upp, ((int64_t)seen + kUnit - 1) / kUnit);
-  const int64_t u0 = (int64_t)split * chunk * 4;
-  const int units = (int)max((int64_t)0, min(listed - u0, (int64_t)chunk * 4));
-  const int tiles = (units + 3) / 4;
-  for (int i = tid; i < 4 * tiles; i += kAtNT) {
-    int blk = -1, pos = 0;
-    if (i < units) {
-      const int64_t u = u0 + i;
-      int slot = (int)(u / upp);
-      const int sub = (int)(u % upp);
-      if (a.ids != nullptr) slot = a.ids[(int64_t)r * a.K + slot];
-      blk = block_of(a, pages, slot, h);
-      if (blk >= 0) pos = slot * a.page_size + sub * kUnit;
-      if (pos >= seen) blk = -1;
-    }
-    u_blk[i] = blk;
-    u_pos[i] = blk < 0 ? 0 : pos;
-  }
-
   const float call_scale = fabsf(a.score_scale);
   const Cap cap(a.softcap);
   at_bf16x8 q[NT][4];
@@ -99,26 +77,51 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   }
   AttnState<NT> st;
   attn_init(st);
-  __syncthreads();
 
-  for (int t = w; t < tiles; t += kAtWaves) {
-    const int ku = 4 * t + (n >> 2), vu = 4 * t + g;
-    const int kblk = u_blk[ku], vblk = u_blk[vu], pos = u_pos[vu];
-    const int have = vblk < 0 ? 0 : min(seen - pos, kUnit);
-    if (__all(have == 0)) continue;
-    // (its scales are asked for with the codes, not while the units are listed: a
-    // workgroup's start is a chain of loads already)
-    uint4 k[4][2], v[8];
-    const float ks = a.k_scale[max(vblk, 0)], vs = a.v_scale[max(vblk, 0)];
-    load_tile(a, kblk, (u_pos[ku] & (a.page_size - 1)) / kUnit, vblk,
-              (pos & (a.page_size - 1)) / kUnit, n, g, k, v);
-    const bool any = !__all(have == kUnit);
-    if (any) {
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
+  // this workgroup's units, list slots or selected slots of 16 tokens each, a phase at a
+  // time
+  const int64_t listed =
+      a.ids != nullptr ? (int64_t)a.K * upp
+                       : min((int64_t)pages.n * upp, ((int64_t)seen + kUnit - 1) / kUnit);
+  const int64_t end = min(listed, ((int64_t)split + 1) * chunk * 4);
+  for (int64_t u0 = (int64_t)split * chunk * 4; u0 < end; u0 += kPhaseUnits) {
+    const int units = (int)min(end - u0, (int64_t)kPhaseUnits);
+    const int tiles = (units + 3) / 4;
+    __syncthreads();  // the phase before has been read
+    for (int i = tid; i < 4 * tiles; i += kAtNT) {
+      int blk = -1, pos = 0;
+      if (i < units) {
+        const int64_t u = u0 + i;
+        int slot = (int)(u / upp);
+        const int sub = (int)(u % upp);
+        if (a.ids != nullptr) slot = a.ids[(int64_t)r * a.K + slot];
+        blk = block_of(a, pages, slot, h);
+        if (blk >= 0) pos = slot * a.page_size + sub * kUnit;
+        if (pos >= seen) blk = -1;
+      }
+      u_blk[i] = blk;
+      u_pos[i] = blk < 0 ? 0 : pos;
     }
-    attn_tile<NT, KIND>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
-                         vblk < 0 ? 0.f : vs, pos, have, len, slope2, cap, any);
+    __syncthreads();
+    for (int t = w; t < tiles; t += kAtWaves) {
+      const int ku = 4 * t + (n >> 2), vu = 4 * t + g;
+      const int kblk = u_blk[ku], vblk = u_blk[vu], pos = u_pos[vu];
+      const int have = vblk < 0 ? 0 : min(seen - pos, kUnit);
+      if (__all(have == 0)) continue;
+      // (its scales are asked for with the codes, not while the units are listed: a
+      // workgroup's start is a chain of loads already)
+      uint4 k[4][2], v[8];
+      const float ks = a.k_scale[max(vblk, 0)], vs = a.v_scale[max(vblk, 0)];
+      load_tile(a, kblk, (u_pos[ku] & (a.page_size - 1)) / kUnit, vblk,
+                (pos & (a.page_size - 1)) / kUnit, n, g, k, v);
+      const bool any = !__all(have == kUnit);
+      if (any) {
+#pragma unroll
+        for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
+      }
+      attn_tile<NT, KIND>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
+                           vblk < 0 ? 0.f : vs, pos, have, len, slope2, cap, any);
+    }
   }
 
   // join the waves
@@ -271,8 +274,7 @@ AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
   int64_t splits = pairs >= 512 ? 1 : (2048 + pairs - 1) / pairs;
   if (splits > tiles / kAtWaves) splits = tiles / kAtWaves;
   if (splits < 1) splits = 1;
-  int64_t chunk = (tiles + splits - 1) / splits;
-  if (chunk > kChunkTiles) chunk = kChunkTiles;
+  const int64_t chunk = (tiles + splits - 1) / splits;
   return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
 }
 

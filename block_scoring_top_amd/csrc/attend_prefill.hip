@@ -40,8 +40,8 @@ namespace {
 constexpr int kPreWaves = 8;
 constexpr int kPreNT = kPreWaves * kWave;
 constexpr int kPreRows = 32 * kPreWaves;
-constexpr int kPreChunk = 512;                // most tiles of a workgroup: page data in LDS
-constexpr int kPreUnits = 4 * (kPreChunk + 4);  // and for the tiles loaded ahead
+constexpr int kPhase = 512;                   // tiles whose page data wait in LDS
+constexpr int kPreUnits = 4 * (kPhase + 4);   // and for the tiles loaded ahead
 constexpr int kAhead = 4;                     // operands read from LDS before their use
 constexpr int kFrag = kWave;                  // uint4s of one operand in LDS
 
@@ -135,7 +135,6 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     lds.longest[w] = longest;
     lds.shortest[w] = shortest;
   }
-  if (tid < 2) lds.nan_tile[tid] = 0;
   __syncthreads();
   int most = 0, least = 0x7FFFFFFF;  // of the workgroup's rows
 #pragma unroll
@@ -145,32 +144,8 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   }
 
   const int units = min(pages.n << ush, (int)(((int64_t)most + kUnit - 1) / kUnit));
-  const int begin = split * chunk;
-  const int count = min((units + 3) / 4 - begin, chunk);  // tiles of this workgroup
-
-  // page data of the tiles, and the largest value scale
-  float vref = 0.f;
-  for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
-    const int u = 4 * begin + i;
-    const int blk = i < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
-    lds.u_blk[i] = blk;
-    lds.u_ks[i] = blk < 0 ? 0.f : a.k_scale[blk] * call_scale;
-    const float vs = blk < 0 ? 0.f : a.v_scale[blk];
-    lds.u_lv[i] = vs;
-    vref = fmaxf(vref, vs);
-  }
-  vref = halves_max(vref);
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) vref = fmaxf(vref, __shfl_xor(vref, d));
-  if (lane == 0) lds.red[w] = vref;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPreWaves; ++i) vref = fmaxf(vref, lds.red[i]);
-  // value scales as logarithms relative to it; below 2^-60 fp16 holds nothing of them
-  for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
-    const float vs = lds.u_lv[i];
-    lds.u_lv[i] = vs == vref ? 0.f : fmaxf(__log2f(vs / vref), -60.f);
-  }
+  const int end = (int)min(((int64_t)units + 3) / 4, ((int64_t)split + 1) * chunk);
+  int begin = 0, count = 0;  // the phase's tiles
 
   // staging: thread -> (token, 16 dims) of the keys and (unit, dim) of the values
   const int64_t block = (int64_t)a.page_size * kHeadDim;
@@ -181,7 +156,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   uint4 kreg, vreg;
   int vhave = 0;  // visible tokens of this thread's value unit
   bool kval = false;
-  auto load_k = [&](int c) {  // c: tile of the workgroup
+  auto load_k = [&](int c) {  // c: tile of the phase
     const int kb = lds.u_blk[4 * c + ku];
     kval = kb >= 0;
     kreg = *reinterpret_cast<const uint4*>(
@@ -232,8 +207,8 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m = -__builtin_inff(), l = 0.f;
+  float vref = 0.f;     // the largest value scale so far: o is in its units
   float ksc[2], lv[2];  // scales of the tile
-  const int mine = (int)min((int64_t)count, ((int64_t)longest + kTileTok - 1) / kTileTok - begin);
 
   // operands are read from LDS kAhead products before their use
   auto products = [&](at_f32x16 (&x)[2], int c) {
@@ -365,7 +340,42 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     }
   };
 
-  if (count > 0) {
+  for (begin = split * chunk; begin < end; begin += kPhase) {
+    count = min(end - begin, kPhase);
+    // the tiles any row of the wave sees
+    const int mine =
+        (int)min((int64_t)count, ((int64_t)longest + kTileTok - 1) / kTileTok - begin);
+    __syncthreads();  // the phase before has been read
+    if (tid < 2) lds.nan_tile[tid] = 0;
+    // page data of the tiles, and the largest value scale
+    float vmax = 0.f;
+    for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
+      const int u = 4 * begin + i;
+      const int blk = i < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
+      lds.u_blk[i] = blk;
+      lds.u_ks[i] = blk < 0 ? 0.f : a.k_scale[blk] * call_scale;
+      const float vs = blk < 0 ? 0.f : a.v_scale[blk];
+      lds.u_lv[i] = vs;
+      vmax = fmaxf(vmax, vs);
+    }
+    vmax = halves_max(vmax);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) vmax = fmaxf(vmax, __shfl_xor(vmax, d));
+    if (lane == 0) lds.red[w] = vmax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPreWaves; ++i) vmax = fmaxf(vmax, lds.red[i]);
+    if (vmax > vref) {
+      const float f = vref / vmax;
+#pragma unroll
+      for (int dt = 0; dt < 4; ++dt) o[dt] *= f;
+      vref = vmax;
+    }
+    // value scales as logarithms relative to it; below 2^-60 fp16 holds nothing of them
+    for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
+      const float vs = lds.u_lv[i];
+      lds.u_lv[i] = vs == vref ? 0.f : fmaxf(__log2f(vs / vref), -60.f);
+    }
     load_k(0);
     load_v(0);
     store_k(0);
@@ -431,8 +441,7 @@ AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t un
   int64_t splits = 1;
   if (most(256, 4) > splits) splits = most(256, 4);
   if (groups < 512 && most(1536, 32) > splits) splits = most(1536, 32);
-  int64_t chunk = (tiles + splits - 1) / splits;
-  if (chunk > kPreChunk) chunk = kPreChunk;
+  const int64_t chunk = (tiles + splits - 1) / splits;
   return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
 }
 

@@ -52,6 +52,8 @@ int check_attend(const void* q, int64_t q_stride, const void* k_cache, const voi
     return IDX_ERR_INVALID_ARG;
   if (dt != IDX_F32 && dt != IDX_BF16) return IDX_ERR_INVALID_ARG;
   if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.f) return IDX_ERR_INVALID_ARG;
+  if (softcap > 0.f && (softcap < IDX_MIN_SOFTCAP || softcap > IDX_MAX_SOFTCAP))
+    return IDX_ERR_UNSUPPORTED;
   if (D != IDX_HEAD_DIM || dt != IDX_BF16 || Hq / Hkv > IDX_MAX_GROUP ||
       !page_size_built(page_size))
     return IDX_ERR_UNSUPPORTED;
@@ -155,7 +157,7 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
   if (dt != IDX_F32 && dt != IDX_BF16) return IDX_ERR_INVALID_ARG;
   if (D != IDX_HEAD_DIM || !page_size_built(page_size)) return IDX_ERR_UNSUPPORTED;
   if ((int64_t)n_pages * Hkv > kMaxInt || (int64_t)n_pages * page_size > kMaxInt ||
-      (int64_t)n_tok * Hkv > kMaxInt || (int64_t)Hkv * D > kMaxInt)
+      (int64_t)n_tok * Hkv > kMaxInt || (int64_t)Hkv * D > kMaxInt || n_tok > 1 << 30)
     return IDX_ERR_INVALID_ARG;
   if (n_tok > 0) {
     if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr ||

@@ -169,10 +169,10 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     const int b = b0 + k;
     int32_t* row = table + (int64_t)b * max_pages;
     // a page taken from the ring in this step
-    auto new_page = [&](int i) {
+    auto new_page = [&](int64_t i) {
       return ring[((int64_t)head + r.grown + (i - r.old_pages)) % n_pages];
     };
-    for (int i = at0; i < r.new_pages; i += step_n) {
+    for (int64_t i = at0; i < r.new_pages; i += step_n) {
       int32_t p;
       if (i < r.old_pages) {
         p = row[i];
@@ -185,16 +185,16 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     }
     // pages given back join the ring behind the free ones (more than the ring has
     // room for can only come from an inconsistent state: they are dropped)
-    for (int i = r.new_pages + at0; i < r.old_pages; i += step_n) {
+    for (int64_t i = (int64_t)r.new_pages + at0; i < r.old_pages; i += step_n) {
       const int64_t j = (int64_t)free_n + r.gave + (i - r.new_pages);
       if (j < n_pages) ring[(head + j) % n_pages] = row[i];
     }
-    for (int i = at0; i < r.fresh; i += step_n) {
+    for (int64_t i = at0; i < r.fresh; i += step_n) {
       const int64_t at = r.tok + i;
       if (at >= n_tok) break;
       int32_t slot = -1, len = 0;
       if (r.served) {
-        const int pos = r.have + i, e = div((uint32_t)pos);
+        const int pos = r.have + (int)i, e = div((uint32_t)pos);
         const int32_t p = e < r.old_pages ? row[e] : new_page(e);
         if (p >= 0 && p < n_pages) {  // else: not an entry that a step handed out
           slot = p * page_size + (pos - e * page_size);

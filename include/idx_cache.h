@@ -31,6 +31,8 @@ extern "C" {
 #endif
 
 #define IDX_MAX_GROUP 64         /* Hq / Hkv of the attention calls               */
+#define IDX_MIN_SOFTCAP 0x1p-20f /* smallest and largest cap of scores: a capped    */
+#define IDX_MAX_SOFTCAP 0x1p16f  /* score is off by up to 2^-20 of the cap          */
 #define IDX_CACHE_MIN_EXP (-120) /* idx_cache_write: no scale below 2^-120        */
 
 /*
@@ -101,7 +103,7 @@ int idx_page_tables(const int32_t* seq_len, const int32_t* n_new, const int32_t*
  *          and the tokens of one page lie in consecutive rows, in order of
  *          their offsets and without gaps; otherwise that page's contents are
  *          unspecified.
- * n_tok >= 0 (0: nothing is enqueued), dt IDX_F32 or IDX_BF16, page_size 16, 32
+ * 0 <= n_tok <= 2^30 (0: nothing is enqueued), dt IDX_F32 or IDX_BF16, page_size 16, 32
  * or 64.
  */
 int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -136,8 +138,11 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * bf16 products; a probability is rounded to 11 bits (fp16) before it meets its
  * value, whose e4m3 code is exact there. That holds while the value scales of
  * one head that matter lie within 2^20 of each other.
- * scale finite; softcap finite, >= 0 (0: none). R >= 0 (0: nothing is enqueued),
+ * scale finite, and the scores finite in fp32; softcap 0 (none) or from
+ * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued),
  * 1 <= Hq / Hkv <= IDX_MAX_GROUP, Hq a multiple of Hkv, page_size 16, 32 or 64.
+ * max_pages may be any bound of the lists' lengths; how rows are cut for the chip goes
+ * by it, so that work spreads best when it is near the longest list.
  * ws: at least idx_attend_workspace_bytes(...) bytes (256-byte aligned; may be
  * NULL when that is 0): partial results of rows split over several workgroups.
  */

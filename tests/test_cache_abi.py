@@ -54,6 +54,7 @@ WRITE = dict(k=P, v=P, k_stride=512, v_stride=512, slots=P, k_cache=P, v_cache=P
     (dict(k_stride=511), INVALID), (dict(v_stride=504), INVALID), (dict(k_stride=516), INVALID),
     (dict(n_tok=-1), INVALID), (dict(Hkv=0), INVALID), (dict(n_pages=0), INVALID),
     (dict(page_size=0), INVALID), (dict(dt=2), INVALID), (dict(n_pages=1 << 30), INVALID),
+    (dict(n_tok=(1 << 30) + 1, Hkv=1), INVALID),
     (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED),
     (dict(page_size=128), UNSUPPORTED), (dict(D=64), UNSUPPORTED),
     (dict(n_tok=0), OK), (dict(n_tok=0, k=None, slots=None), OK),
@@ -78,6 +79,7 @@ SHARED = [
     (dict(max_pages=1 << 28), INVALID), (dict(n_pages=1 << 30), INVALID),
     (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
     (dict(softcap=-1.0), INVALID), (dict(softcap=math.nan), INVALID), (dict(dt=2), INVALID),
+    (dict(softcap=1e-30), UNSUPPORTED), (dict(softcap=1e6), UNSUPPORTED),
     (dict(dt=0), UNSUPPORTED), (dict(D=64), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED),
     (dict(page_size=24), UNSUPPORTED), (dict(Hq=65 * 4, q_stride=65 * 512), UNSUPPORTED),
 ]
@@ -111,7 +113,7 @@ def test_attend_prefill_rejects(lib, kw, want):
 def test_workspace_sizes(lib):
     # none where a row is not cut; else, per row and head, the same count of partial
     # results: 128 sums and two statistics
-    assert lib.idx_attend_workspace_bytes(2, 16, 4, 32, 0, 16) == 0
+    assert lib.idx_attend_workspace_bytes(2, 16, 4, 8, 0, 16) == 0
     assert lib.idx_attend_workspace_bytes(0, 16, 4, 4096, 0, 16) == 0
     assert lib.idx_attend_workspace_bytes(4, 17, 4, 4096, 0, 16) == 0   # not a legal shape
     n = lib.idx_attend_workspace_bytes(2, 16, 4, 4096, 0, 16)
@@ -119,6 +121,13 @@ def test_workspace_sizes(lib):
     n = lib.idx_attend_prefill_workspace_bytes(3, 2, 16, 4, 4096, 16)
     assert n > 0
     assert lib.idx_attend_prefill_workspace_bytes(3, 2, 16, 4, 1, 16) == 0
+
+
+def test_workspaces_do_not_grow_with_a_generous_bound(lib):
+    for pages in (4096, 1 << 18, 1 << 24):
+        assert lib.idx_attend_workspace_bytes(4, 16, 4, pages, 0, 16) <= 4 * 16 * 128 * 521
+        assert lib.idx_attend_workspace_bytes(512, 16, 4, pages, 0, 16) == 0
+        assert lib.idx_attend_prefill_workspace_bytes(8192, 2, 16, 4, pages, 16) == 0
 
 
 def test_binding_refuses_tensors_off_the_gpu():

@@ -508,6 +508,24 @@ def test_prefill_long_contexts_over_several_workgroups(lens, news):
     check_rows(prefill(c, q, ptr, seen), c, q64, req, seen)
 
 
+def test_bounds_far_above_the_lists():
+    """max_pages far above the longest list, and rows longer than one phase of page data
+    (16384 tokens of single tokens' rows, 32768 of prompt rows)."""
+    lens, news = [300, 45], [60, 5]
+    c = Cache(52, lens, 1, 16, max_pages=1 << 18)
+    ptr, req, seen = causal(lens, news)
+    q, q64 = queries(c.rng, len(req), 4)
+    check_rows(prefill(c, q, ptr, seen), c, q64, req, seen)
+    check_rows(attend(c, q, seen, row_req=i32(req)), c, q64, req, seen)
+    lens = [70001]
+    c = Cache(53, lens, 1, 16, max_pages=1 << 22)
+    c.vs[c.indices, 0] = np.exp2(np.linspace(-9, -3, len(c.indices))).astype(np.float32)
+    ptr, req, seen = causal(lens, [30])
+    q, q64 = queries(c.rng, 30, 4)
+    check_rows(prefill(c, q, ptr, seen), c, q64, req, seen, rows=[0, 7, 29])
+    check_rows(attend(c, q, seen, row_req=i32(req)), c, q64, req, seen, rows=[0, 7, 29])
+
+
 def test_prefill_bad_pages():
     lens = [160, 160]
     c = Cache(48, lens, 2, 16)
