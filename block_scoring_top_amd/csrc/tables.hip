@@ -25,7 +25,7 @@ namespace {
 constexpr int kTabOwn = 64;  // most requests of one workgroup
 
 struct TabReq {
-  int64_t tok;          // first token row
+  uint32_t tok;         // first token row
   int have, after;      // tokens before and after the step
   int old_pages, new_pages;
   int grown, gave;      // first new page, first page given back
@@ -34,37 +34,53 @@ struct TabReq {
   bool served;
 };
 
+// Sums that stop at 2^32 - 1 (a count of token rows past every array, when they do);
+// where no sum gets there they are the plain ones.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+  return __builtin_elementwise_add_sat(a, b);
+}
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ uint32_t scan_step(uint32_t v) {
+  return add_sat(v, dpp_u32<CTRL, ROW_MASK>(v));
+}
+__device__ __forceinline__ uint32_t wave_scan_sat(uint32_t v) {
+  v = scan_step<kDppRowShr1>(v);
+  v = scan_step<kDppRowShr1 + 1>(v);
+  v = scan_step<kDppRowShr1 + 3>(v);
+  v = scan_step<kDppRowShr1 + 7>(v);
+  v = scan_step<kDppRowBcast15, 0xA>(v);
+  return scan_step<kDppRowBcast31, 0xC>(v);
+}
+
 // Exclusive prefix sums over the workgroup's threads of N values at once; v becomes the
-// sum of the threads before, total that of all.
-template <int NT, int N, typename T>
-__device__ __forceinline__ void block_scan(T (&v)[N], T (*lds)[NT / kWave], T (&total)[N]) {
-  const int lane = lane_id(), w = threadIdx.x / kWave;
-  T own[N];
+// sum of the threads before, total that of all. The waves' sums are scanned by every wave
+// for itself, a lane for each.
+template <int NT, int N>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (*lds)[NT / kWave],
+                                           uint32_t (&total)[N]) {
+  constexpr int WAVES = NT / kWave;
+  static_assert(WAVES <= 16, "the waves' sums lie in one row of lanes");
+  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  uint32_t sum[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) own[i] = v[i];
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const T o = __shfl_up(v[i], d);
-      if (lane >= d) v[i] += o;
-    }
+  for (int i = 0; i < N; ++i) sum[i] = wave_scan_sat(v[i]);
   __syncthreads();  // the previous sums have been read
   if (lane == kWave - 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) lds[i][w] = v[i];
+    for (int i = 0; i < N; ++i) lds[i][w] = sum[i];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    T before = 0;
-    total[i] = 0;
-#pragma unroll
-    for (int j = 0; j < NT / kWave; ++j) {
-      const T s = lds[i][j];
-      before += j < w ? s : 0;
-      total[i] += s;
-    }
-    v[i] += before - own[i];
+    uint32_t s = lane < WAVES ? lds[i][lane] : 0;
+    s = scan_step<kDppRowShr1>(s);
+    s = scan_step<kDppRowShr1 + 1>(s);
+    s = scan_step<kDppRowShr1 + 3>(s);
+    s = scan_step<kDppRowShr1 + 7>(s);
+    total[i] = readlane<uint32_t>(s, WAVES - 1);
+    const uint32_t before = w == 0 ? 0 : readlane<uint32_t>(s, w - 1);
+    // this thread's inclusive sum less its own value: the neighbour's, in the same wave
+    const uint32_t left = (uint32_t)__shfl_up((int)sum[i], 1);
+    v[i] = add_sat(before, lane == 0 ? 0 : left);
   }
 }
 
@@ -79,8 +95,7 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     int32_t* __restrict__ tok_req, int32_t* __restrict__ tok_len, int B, int max_pages,
     int page_size, int n_pages, int64_t n_indices, int n_tok, int own,
     int shift) {
-  __shared__ int64_t lds64[1][NT / kWave];
-  __shared__ int lds32[4][NT / kWave];
+  __shared__ uint32_t lds[4][NT / kWave];
   __shared__ TabReq mine[kTabOwn];
   const int tid = threadIdx.x;
   const int b0 = blockIdx.x * own, b1 = min(b0 + own, B);
@@ -102,29 +117,30 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
   };
   auto pages = [&](int tokens) { return div((uint32_t)tokens + (page_size - 1)); };
 
-  int64_t tok[1] = {0}, total_tok[1];
+  uint32_t tok[1] = {0}, total_tok[1];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) tok[0] += max(change[i], 0);
-  block_scan<NT>(tok, lds64, total_tok);
+  for (int i = 0; i < PER; ++i) tok[0] = add_sat(tok[0], max(change[i], 0));
+  block_scan<NT>(tok, lds, total_tok);
 
   // pages needed; -1 marks a request that cannot be served whatever is free
-  int need[PER], sum[1] = {0}, total_need[1];
-  int64_t t = tok[0];
+  int need[PER];
+  uint32_t sum[1] = {0}, total_need[1];
+  uint32_t t = tok[0];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    t += max(change[i], 0);
+    t = add_sat(t, max(change[i], 0));
     const int64_t after = max((int64_t)have[i] + change[i], (int64_t)0);
-    const bool fits = after <= most && (change[i] <= 0 || t <= n_tok);
+    const bool fits = after <= most && (change[i] <= 0 || t <= (uint32_t)n_tok);
     need[i] = fits ? max(pages((int)after) - pages(have[i]), 0) : -1;
     sum[0] += max(need[i], 0);
   }
-  block_scan<NT>(sum, lds32, total_need);
+  block_scan<NT>(sum, lds, total_need);
 
-  int v[4] = {0, 0, 0, 0}, total[4];  // pages held, given back, taken; requests refused
-  int n = sum[0];
+  uint32_t v[4] = {0, 0, 0, 0}, total[4];  // pages held, given back, taken; refused
+  uint32_t n = sum[0];
   auto step = [&](int i, int& after, int& np) {  // whether request i is served
     n += max(need[i], 0);
-    const bool served = need[i] == 0 || (need[i] > 0 && n <= free_n);
+    const bool served = need[i] == 0 || (need[i] > 0 && n <= (uint32_t)free_n);
     after = served ? (int)max((int64_t)have[i] + change[i], (int64_t)0) : have[i];
     np = pages(after);
     return served;
@@ -138,7 +154,7 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     v[2] += served ? need[i] : 0;
     v[3] += !served && tid * PER + i < B ? 1 : 0;
   }
-  block_scan<NT>(v, lds32, total);
+  block_scan<NT>(v, lds, total);
 
   // the prefixes of this workgroup's own requests
   if (tid * PER < b1 && (tid + 1) * PER > b0) {
@@ -146,13 +162,13 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     n = sum[0];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int b = tid * PER + i, grown = n;
+      const int b = tid * PER + i, grown = (int)n;
       int after, np;
       const bool served = step(i, after, np);
       if (b >= b0 && b < b1)
-        mine[b - b0] = TabReq{t,     have[i], after, pages(have[i]), np, grown, v[1], v[0],
-                              (int)min((int64_t)max(change[i], 0), (int64_t)n_tok), served};
-      t += max(change[i], 0);
+        mine[b - b0] = TabReq{t,  have[i], after,     pages(have[i]), np, grown, (int)v[1],
+                              (int)v[0], min(max(change[i], 0), n_tok), served};
+      t = add_sat(t, max(change[i], 0));
       v[0] += np;
       v[1] += max(pages(have[i]) - np, 0);
     }
@@ -190,7 +206,7 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
       if (j < n_pages) ring[(head + j) % n_pages] = row[i];
     }
     for (int64_t i = at0; i < r.fresh; i += step_n) {
-      const int64_t at = r.tok + i;
+      const int64_t at = (int64_t)r.tok + i;
       if (at >= n_tok) break;
       int32_t slot = -1, len = 0;
       if (r.served) {
@@ -208,23 +224,24 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     if (lead) {
       seq_out[b] = r.after;
       kv_indptr[b] = r.kv;
-      tok_indptr[b] = (int32_t)min(r.tok, (int64_t)n_tok);
+      tok_indptr[b] = (int32_t)min(r.tok, (uint32_t)n_tok);
     }
   }
   // the rows past the last token, and what belongs to no request
   if (blockIdx.x == gridDim.x - 1)
-    for (int64_t i = min(total_tok[0], (int64_t)n_tok) + blockIdx.y * NT + tid; i < n_tok;
+    for (int64_t i = min(total_tok[0], (uint32_t)n_tok) + blockIdx.y * NT + tid; i < n_tok;
          i += gridDim.y * NT) {
       slots[i] = -1;
       tok_req[i] = -1;
       tok_len[i] = 0;
     }
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
-    kv_indptr[B] = total[0];
-    tok_indptr[B] = (int32_t)min(total_tok[0], (int64_t)n_tok);
+    kv_indptr[B] = (int32_t)total[0];
+    tok_indptr[B] = (int32_t)min(total_tok[0], (uint32_t)n_tok);
     cursor_out[0] = (int32_t)(((int64_t)head + total[2]) % n_pages);
-    cursor_out[1] = (int32_t)min((int64_t)free_n - total[2] + total[1], (int64_t)n_pages);
-    cursor_out[2] = total[3];
+    cursor_out[1] =
+        (int32_t)min((int64_t)free_n - total[2] + (int64_t)total[1], (int64_t)n_pages);
+    cursor_out[2] = (int32_t)total[3];
   }
 }
 
@@ -237,7 +254,7 @@ int launch_page_tables(const int32_t* seq_len, const int32_t* n_new, const int32
                        int page_size, int n_pages, int64_t n_indices, int n_tok, void* stream) {
   // up to 256 requests: one thread and one workgroup (or several) for each; more: a
   // wave for each, 256 workgroups running the sums (4096 requests: 65 us with a
-  // workgroup of 256 threads for each four, which reread the lengths, 16.6 so)
+  // workgroup of 256 threads for each four, which reread the lengths, 13 so)
   const int own = B <= 256 ? 1 : (B + 255) / 256;
   const int gx = (B + own - 1) / own;
   int gy = 1;  // a few requests: several workgroups for each
