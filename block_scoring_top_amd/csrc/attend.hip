@@ -216,8 +216,16 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
         const int s = s0 + i * TEAMS;
         const int64_t p = first + (int64_t)min(s, splits - 1) * G;
         ml[i] = *reinterpret_cast<const at_f32x2*>(a.part_ml + 2 * p);
-        x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
         if (s >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
+      }
+      // (a split without tokens leaves its sums unwritten)
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};
+        if (ml[i][1] != 0.f) {
+          const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
+          x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
+        }
       }
       float top = m;
 #pragma unroll
@@ -229,7 +237,6 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
       o *= f;
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
-        if (ml[i][1] == 0.f) continue;  // a split without tokens: its sums are not written
         const float w = exp2_fast(ml[i][0] - base);
         l += ml[i][1] * w;
         o += x[i] * w;
@@ -267,7 +274,8 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
 // batch of 128 rows on 4 heads, 256 pages each: 102 us whole, 108 in two). Then into
 // chunks that would give eight a CU if all rows were of the longest length, so that
 // ragged rows still balance (4 rows of 4096 to 131072 tokens on 8 heads: 148 us at two a
-// CU, 136 at four, 123 at eight, 127 at sixteen), down to a tile for each wave.
+// CU, 136 at four, 123 at eight, 127 at sixteen; equal shares for all that the chip holds at
+// once, worked out by the kernel, are slower, 130), down to a tile for each wave.
 AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
   const int64_t tiles = (units + 3) / 4;
   const int64_t pairs = R * Hkv;

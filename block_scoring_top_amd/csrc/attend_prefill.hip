@@ -40,6 +40,7 @@ namespace {
 constexpr int kPreWaves = 8;
 constexpr int kPreNT = kPreWaves * kWave;
 constexpr int kPreRows = 32 * kPreWaves;
+constexpr int kCUs = 256;
 constexpr int kPhase = 512;                   // tiles whose page data wait in LDS
 constexpr int kPreUnits = 4 * (kPhase + 4);   // and for the tiles loaded ahead
 constexpr int kAhead = 4;                     // operands read from LDS before their use
@@ -52,6 +53,7 @@ struct PreLds {
   float u_ks[kPreUnits], u_lv[kPreUnits];
   float red[kPreWaves];
   int longest[kPreWaves], shortest[kPreWaves];
+  unsigned long long work[kPreWaves];
   // NaN value codes of a tile that some rows see only in part: which tile (plus one),
   // and for each dim and unit which of its 16 tokens
   int nan_tile[2];
@@ -131,20 +133,45 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     longest = max(longest, __shfl_xor(longest, d));
     shortest = min(shortest, __shfl_xor(shortest, d));
   }
+  // A cut call's stretches: the host knows only a bound of the lengths and cuts for that;
+  // where the lengths give less than a stretch to each CU of that size, longer ones, equal
+  // to a CU's share of the call, end together (and leave fewer partial sums). The work is
+  // the requests' row tiles times the mean of their first and last row's tiles.
+  unsigned long long work = 0;
+  if (splits > 1) {
+    for (int i = tid; i < a.B; i += kPreNT) {
+      const int x0 = min(max(a.tok_indptr[i], 0), a.R);
+      const int x1 = min(max(a.tok_indptr[i + 1], 0), a.R);
+      if (x1 <= x0) continue;
+      const int64_t held = (int64_t)page_list(a, i).n * a.page_size;
+      const int64_t seen = min(held, (int64_t)max(a.kv_len[x0], 0)) +
+                           min(held, (int64_t)max(a.kv_len[x1 - 1], 0));
+      work += (((int64_t)(x1 - x0) * G + kPreRows - 1) / kPreRows) *
+              ((seen / 2 + kTileTok - 1) / kTileTok);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) work += __shfl_xor(work, d);
+  }
   if (lane == 0) {
     lds.longest[w] = longest;
     lds.shortest[w] = shortest;
+    lds.work[w] = work;
   }
   __syncthreads();
   int most = 0, least = 0x7FFFFFFF;  // of the workgroup's rows
+  work = 0;
 #pragma unroll
   for (int i = 0; i < kPreWaves; ++i) {
     most = max(most, lds.longest[i]);
     least = min(least, lds.shortest[i]);
+    work += lds.work[i];
   }
+  if (splits > 1)
+    chunk = (int)min((unsigned long long)0x7FFFFFFF,
+                     max((unsigned long long)chunk, (work * a.Hkv + kCUs - 1) / kCUs));
 
   const int units = min(pages.n << ush, (int)(((int64_t)most + kUnit - 1) / kUnit));
-  const int end = (int)min(((int64_t)units + 3) / 4, ((int64_t)split + 1) * chunk);
+  const int64_t end = min(((int64_t)units + 3) / 4, ((int64_t)split + 1) * chunk);
   int begin = 0, count = 0;  // the phase's tiles
 
   // staging: thread -> (token, 16 dims) of the keys and (unit, dim) of the values
@@ -340,8 +367,9 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     }
   };
 
-  for (begin = split * chunk; begin < end; begin += kPhase) {
-    count = min(end - begin, kPhase);
+  for (int64_t at = (int64_t)split * chunk; at < end; at += kPhase) {
+    begin = (int)at;
+    count = (int)min(end - at, (int64_t)kPhase);
     // the tiles any row of the wave sees
     const int mine =
         (int)min((int64_t)count, ((int64_t)longest + kTileTok - 1) / kTileTok - begin);
@@ -425,12 +453,13 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 
 int64_t attend_prefill_tiles(int64_t n_tok, int B, int G) { return n_tok * G / kPreRows + B; }
 
-// A call of fewer than two workgroups a CU is cut along its keys into about 1536, but not
-// below 32 tiles each: a workgroup's start and end cost four tiles' time, and its partial
-// sums are written and read again (chunks of 512 tokens on 4608 and 30512, 32 heads on 8:
-// 492 us at 512 wanted, 484 at 1536; the two prompts of 8192, 2032 workgroups: 1.14 ms
-// whole, 1.42 in two). One of fewer workgroups than CUs goes down to four tiles (five
-// tokens on 900 to 2777: 29 us at eight, 22 so).
+// A call of fewer than two workgroups a CU is cut along its keys, into at most so many
+// stretches as give about 512 workgroups of no less than 32 tiles; one of fewer workgroups
+// than CUs down to four tiles (five tokens on 900 to 2777: 29 us at eight, 22 so). A
+// workgroup's start and end cost four tiles' time, and its partial sums are written and
+// read again (the two prompts of 8192, 2032 workgroups: 1.14 ms whole, 1.42 in two). The
+// kernel lengthens the stretches to a CU's share of the call: chunks of 512 tokens on 4608
+// and 30512, 32 heads on 8, 492 us before that and 418 so, 433 at 1024 wanted.
 AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
   const int64_t tiles = (units + 3) / 4;
   const int64_t groups = attend_prefill_tiles(n_tok, B, Hq / Hkv) * Hkv;
@@ -440,7 +469,7 @@ AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t un
   };
   int64_t splits = 1;
   if (most(256, 4) > splits) splits = most(256, 4);
-  if (groups < 512 && most(1536, 32) > splits) splits = most(1536, 32);
+  if (most(512, 32) > splits) splits = most(512, 32);
   const int64_t chunk = (tiles + splits - 1) / splits;
   return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
 }
