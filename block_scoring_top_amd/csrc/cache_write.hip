@@ -12,6 +12,9 @@
 // its key written in whole lines, the run's largest value takes one reduction over the
 // wave, and the four tokens of a lane are one word of the transposed value page, in
 // registers. Everything is read once: the run waits in registers for its scale.
+// 56800 tokens of 8 heads (bf16, 349 MB in and out): 81 us, 4.3 TB/s (a large copy runs at
+// 4.9); 4009 of them 10.3 us, a chain of loads, and 55 with a workgroup for each row and
+// head that reads its elements twice; 128 single tokens of 4 heads 6.0 us.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -212,7 +215,8 @@ int launch_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v
                        const int32_t* slots, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
                        float* v_scale, int n_tok, int Hkv, int n_pages, int page_size, bool bf16,
                        void* stream) {
-  // prompts: a wave looks for runs among 16 rows; a few tokens: a wave for each row
+  // prompts: a wave looks for runs among 16 rows (the 56800 tokens: 81 us, 97 with 8 rows,
+  // 295 with one, 84 with 32); a few tokens: a wave for each row
   const int item_groups = (2 * Hkv + kWrWaves - 1) / kWrWaves;
   const int span = (int64_t)n_tok * item_groups > 8192 ? 16 : 1;
   const int64_t grid = (int64_t)((n_tok + span - 1) / span) * item_groups;
