@@ -2,7 +2,8 @@
 // idx_attend), and the join of partial results. The tile is in attend.hpp.
 //
 // One token's query heads of one KV head are the 16 or 32 rows of the products (above 32
-// heads a group, two workgroups take 32 each).
+// heads a group, two workgroups take 32 each); or, for prompt calls of few rows a request,
+// 16 rows (token, head) of the request.
 // Bound by reading the cache, 256 bytes a token and KV head: each of a workgroup's four
 // waves runs its own tiles, with its own softmax, joined in LDS at the end. Long rows are
 // cut into chunks of tiles for several workgroups; their partial sums are joined by
@@ -42,7 +43,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, int kblk, int ksub,
     v[dt] = *reinterpret_cast<const uint4*>(vp + (int64_t)dt * 16 * a.page_size);
 }
 
-template <int NT, int KIND>
+template <int NT, int KIND, bool PACKED>
 __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int chunk, int splits,
                                                                int bands) {
   __shared__ int u_blk[kPhaseUnits], u_pos[kPhaseUnits];
@@ -52,28 +53,55 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   const int band = blockIdx.x % bands;  // of 16 NT query heads of the group
   const int h = blockIdx.x / bands % a.Hkv;
   const int rest = blockIdx.x / bands / a.Hkv;
-  const int split = rest % splits, r = rest / splits;
+  const int split = rest % splits, r = rest / splits;  // packed: r is a row tile
   const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
   const int n = lane & 15, g = lane >> 4;
   const int G = a.Hq / a.Hkv;
   const int upp = a.page_size / kUnit;
 
-  int b = a.row_req == nullptr ? r : a.row_req[r];
-  const bool known = b >= 0 && b < a.B;
-  const PageList pages = known ? page_list(a, b) : PageList{0, 0};
-  const int seen = known ? max(a.kv_len[r], 0) : 0;
+  // The request, and where row i of this workgroup's 16 NT lies: token row and head of the
+  // group; rows past the last repeat it.
+  RowTile rt{0, r, 16 * NT * band, G};
+  bool known = true;
+  if constexpr (PACKED) {
+    rt = row_tile(a, r, G, 16 * NT);
+    if (rt.row0 < 0 || rt.row0 >= rt.rows) return;
+  } else {
+    rt.b = a.row_req == nullptr ? r : a.row_req[r];
+    known = rt.b >= 0 && rt.b < a.B;
+  }
+  const int rows = (int)min((int64_t)16 * NT, rt.rows - rt.row0);
+  auto token_of = [&](int i) {
+    return PACKED ? rt.t0 + (rt.row0 + min(i, rows - 1)) / G : (int64_t)r;
+  };
+  auto head_of = [&](int i) {
+    const int64_t at = rt.row0 + min(i, rows - 1);
+    return (int)(PACKED ? at % G : at);
+  };
+  const PageList pages = known ? page_list(a, rt.b) : PageList{0, 0};
 
   const float call_scale = fabsf(a.score_scale);
   const Cap cap(a.softcap);
   at_bf16x8 q[NT][4];
   float slope2[NT];
   int len[NT];
+  int seen = 0, shortest = 0x7FFFFFFF;  // longest and shortest visible length of the rows
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int hq = h * G + min(16 * NT * band + 16 * j + n, G - 1);
-    load_query(a.q + (int64_t)r * a.q_stride + hq * kHeadDim, g, a.score_scale < 0.f, q[j]);
+    const int64_t tok = token_of(16 * j + n);
+    const int hq = h * G + head_of(16 * j + n);
+    load_query(a.q + tok * a.q_stride + hq * kHeadDim, g, a.score_scale < 0.f, q[j]);
     slope2[j] = KIND != kPlain ? slope_of(a, hq) : 0.f;
-    len[j] = seen;
+    len[j] = known ? max(a.kv_len[tok], 0) : 0;
+    seen = max(seen, len[j]);
+    shortest = min(shortest, len[j]);
+  }
+  if constexpr (PACKED) {
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+      seen = max(seen, __shfl_xor(seen, d));
+      shortest = min(shortest, __shfl_xor(shortest, d));
+    }
   }
   AttnState<NT> st;
   attn_init(st);
@@ -114,13 +142,9 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
       const float ks = a.k_scale[max(vblk, 0)], vs = a.v_scale[max(vblk, 0)];
       load_tile(a, kblk, (u_pos[ku] & (a.page_size - 1)) / kUnit, vblk,
                 (pos & (a.page_size - 1)) / kUnit, n, g, k, v);
-      const bool any = !__all(have == kUnit);
-      if (any) {
-#pragma unroll
-        for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
-      }
-      attn_tile<NT, KIND>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
-                           vblk < 0 ? 0.f : vs, pos, have, len, slope2, cap, any);
+      const bool any = !__all(have == kUnit && (!PACKED || pos + kUnit <= shortest));
+      attn_tile<NT, KIND, PACKED>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
+                                  vblk < 0 ? 0.f : vs, pos, have, len, slope2, cap, any);
     }
   }
 
@@ -155,10 +179,10 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
     }
     __syncthreads();
   }
-  const int64_t part = ((int64_t)r * a.Hkv + h) * splits + split;
-  const int rows = min(16 * NT, G - 16 * NT * band);
   for (int item = tid; item < rows * 16; item += kAtNT) {
-    const int row = item >> 4, d = (item & 15) * 8, g_row = 16 * NT * band + row;
+    const int row = item >> 4, d = (item & 15) * 8, g_row = head_of(row);
+    const int64_t tok = token_of(row);
+    const int64_t part = (((tok * a.Hkv + h) * splits) + split) * G + g_row;
     float m = s_m[0][row], l = 0.f;
 #pragma unroll
     for (int i = 1; i < kAtWaves; ++i) m = fmaxf(m, s_m[i][row]);
@@ -173,14 +197,14 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
       out.y = pack_bf16(o[2] * inv, o[3] * inv);
       out.z = pack_bf16(o[4] * inv, o[5] * inv);
       out.w = pack_bf16(o[6] * inv, o[7] * inv);
-      *reinterpret_cast<uint4*>(a.out + ((int64_t)r * a.Hq + h * G + g_row) * kHeadDim + d) = out;
+      *reinterpret_cast<uint4*>(a.out + (tok * a.Hq + h * G + g_row) * kHeadDim + d) = out;
     } else {
-      at_f32x4* p = reinterpret_cast<at_f32x4*>(a.part_o + (part * G + g_row) * kHeadDim + d);
+      at_f32x4* p = reinterpret_cast<at_f32x4*>(a.part_o + part * kHeadDim + d);
       p[0] = *reinterpret_cast<const at_f32x4*>(o);
       p[1] = *reinterpret_cast<const at_f32x4*>(o + 4);
       if (d == 0) {
-        a.part_ml[2 * (part * G + g_row)] = m;
-        a.part_ml[2 * (part * G + g_row) + 1] = l;
+        a.part_ml[2 * part] = m;
+        a.part_ml[2 * part + 1] = l;
       }
     }
   }
@@ -283,7 +307,7 @@ AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
   if (splits > tiles / kAtWaves) splits = tiles / kAtWaves;
   if (splits < 1) splits = 1;
   const int64_t chunk = (tiles + splits - 1) / splits;
-  return {(int)chunk, (int)((tiles + chunk - 1) / chunk)};
+  return {(int)chunk, (int)((tiles + chunk - 1) / chunk), 0};
 }
 
 int launch_attend_merge(const AttnArgs& a, int splits, void* stream) {
@@ -304,19 +328,23 @@ int launch_attend_merge(const AttnArgs& a, int splits, void* stream) {
 int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int G = a.Hq / a.Hkv;
-  const int bands = G <= 32 ? 1 : 2;
-  const dim3 grid((unsigned)((int64_t)a.R * a.Hkv * sp.splits * bands)), blk(kAtNT);
-#define IDX_ROWS(NT, KIND)                                                                      \
-  hipLaunchKernelGGL((attend_rows_kernel<NT, KIND>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
-                     bands)
-#define IDX_KINDS(NT)                                \
-  if (a.softcap > 0.f) IDX_ROWS(NT, kCapped);        \
-  else if (a.slopes != nullptr) IDX_ROWS(NT, kBiased); \
-  else IDX_ROWS(NT, kPlain)
-  if (G <= 16) {
-    IDX_KINDS(1);
+  const bool packed = a.tok_indptr != nullptr;
+  const int bands = packed || G <= 32 ? 1 : 2;
+  const int64_t rows = packed ? attend_prefill_tiles(a.R, a.B, G, sp.rows) : a.R;
+  const dim3 grid((unsigned)(rows * a.Hkv * sp.splits * bands)), blk(kAtNT);
+#define IDX_ROWS(NT, KIND, PACKED)                                                              \
+  hipLaunchKernelGGL((attend_rows_kernel<NT, KIND, PACKED>), grid, blk, 0, s, a, sp.chunk, \
+                     sp.splits, bands)
+#define IDX_KINDS(NT, PACKED)                                  \
+  if (a.softcap > 0.f) IDX_ROWS(NT, kCapped, PACKED);          \
+  else if (a.slopes != nullptr) IDX_ROWS(NT, kBiased, PACKED); \
+  else IDX_ROWS(NT, kPlain, PACKED)
+  if (packed) {
+    IDX_KINDS(1, true);
+  } else if (G <= 16) {
+    IDX_KINDS(1, false);
   } else {
-    IDX_KINDS(2);
+    IDX_KINDS(2, false);
   }
 #undef IDX_KINDS
 #undef IDX_ROWS

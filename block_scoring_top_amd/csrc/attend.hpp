@@ -140,15 +140,79 @@ __device__ __forceinline__ void load_query(const uint16_t* row, int g, bool nega
     }
 }
 
+// zeroes the codes of the tokens from `have` on (whatever they hold, NaN included,
+// they would meet a probability of zero)
+__device__ __forceinline__ uint4 keep_tokens(uint4 v, int have) {
+  auto word = [&](uint32_t w, int first) -> uint32_t {
+    const int n = have - first;
+    return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
+  };
+  return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
+}
+
+// Whether a code is NaN: low seven bits all set.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// In a tile that some rows see only in part, a NaN value code must reach the rows that
+// see its token and no others, though all rows share the product (0 x NaN = NaN).
+// Replaces NaN codes by zero and puts NaN into the sums of the rows that see them: the
+// product of "code is NaN" with "row sees token" is positive exactly there.
+template <int NT>
+__device__ __forceinline__ void attn_nan_values(AttnState<NT>& st, uint4 (&v)[8], int pos,
+                                                int have, const int (&len)[NT]) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt)
+    bad |= nan_codes(v[dt].x) | nan_codes(v[dt].y) | nan_codes(v[dt].z) | nan_codes(v[dt].w);
+  if (!__any(bad != 0)) return;
+  uint4 sees[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    uint32_t w[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      auto one = [&](int tok) { return tok < have && pos + tok < len[j] ? 0x3C00u : 0u; };
+      w[t] = one(2 * t) | (one(2 * t + 1) << 16);
+    }
+    sees[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
+    sees[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt) {
+    uint32_t w[4] = {v[dt].x, v[dt].y, v[dt].z, v[dt].w}, is[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t n = nan_codes(w[e]) >> 7;  // 1 in each NaN byte
+      is[e] = n * 0x38u;                        // e4m3 1.0 there
+      w[e] &= ~(n * 0xFFu);
+    }
+    v[dt] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      at_f32x4 hit = {0.f, 0.f, 0.f, 0.f};
+      hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          codes_f16x8(is[0], is[1]), __builtin_bit_cast(at_f16x8, sees[j][0]), hit, 0, 0, 0);
+      hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          codes_f16x8(is[2], is[3]), __builtin_bit_cast(at_f16x8, sees[j][1]), hit, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (hit[i] > 0.f) st.o[j][dt][i] = __builtin_nanf("");
+    }
+    __builtin_amdgcn_sched_barrier(0);  // a rare path: no registers for it
+  }
+}
+
 // One tile. k: this lane's key bytes, k[s][c] = dims 64 c + 16 g .. + 15 of token
 // 4 s + m % 4 of unit m / 4; v[dt]: the 16 tokens of unit g at dim 16 dt + n.
 // ksc: the score scale of unit g; vs: its value scale, 0 if it holds no token; pos:
 // position of its first token; have: how many of its tokens exist; len: visible length
 // of each of the lane's query rows; any: whether a token of the tile is masked for any
-// row (uniform over the wave).
-template <int NT, int KIND>
+// row (uniform over the wave). MIXED: the rows' visible lengths differ.
+template <int NT, int KIND, bool MIXED>
 __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q)[NT][4],
-                                          const uint4 (&k)[4][2], const uint4 (&v)[8], float ksc,
+                                          const uint4 (&k)[4][2], uint4 (&v)[8], float ksc,
                                           float vs, int pos, int have, const int (&len)[NT],
                                           const float (&slope2)[NT], const Cap& cap, bool any) {
   const float vtop = groups_max(vs);
@@ -226,6 +290,12 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
     p[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
     st.l[j] = __builtin_fmaf(sum[0] + sum[1], unlv, st.l[j]);
   }
+  // (values of tokens that no row sees: whatever they hold, it would meet a zero)
+  if (any) {
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt) v[dt] = keep_tokens(v[dt], have);
+    if constexpr (MIXED) attn_nan_values<NT>(st, v, pos, have, len);
+  }
 #pragma unroll
   for (int dt = 0; dt < 8; ++dt) {
     const at_f16x8 v0 = codes_f16x8(v[dt].x, v[dt].y);
@@ -238,21 +308,6 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
           v1, __builtin_bit_cast(at_f16x8, p[j][1]), st.o[j][dt], 0, 0, 0);
     }
   }
-}
-
-// zeroes the codes of the tokens from `have` on (whatever they hold, NaN included,
-// they would meet a probability of zero)
-__device__ __forceinline__ uint4 keep_tokens(uint4 v, int have) {
-  auto word = [&](uint32_t w, int first) -> uint32_t {
-    const int n = have - first;
-    return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
-  };
-  return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
-}
-
-// Whether a code is NaN: low seven bits all set.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
 // The page list of a request.
@@ -277,6 +332,34 @@ __device__ __forceinline__ int block_of(const AttnArgs& a, const PageList& p, in
 
 __device__ __forceinline__ float slope_of(const AttnArgs& a, int hq) {
   return a.slopes == nullptr ? 0.f : a.slopes[hq] * kLog2e;
+}
+
+// Row tiles of packed tokens: `per` rows (token, head of the group) of one request each.
+// Request b's first is floor(rows before it / per) + b: floor(y / T) - floor(x / T) + 1
+// tiles hold any x..y rows, so tiles never span requests.
+__device__ __forceinline__ int64_t first_tile(const AttnArgs& a, int b, int G, int per) {
+  const int64_t p = min(max(a.tok_indptr[b], 0), a.R);
+  return p * G / per + b;
+}
+struct RowTile {
+  int b, t0;           // request and its first token row
+  int64_t row0, rows;  // first row of the tile, rows of the request (0 <= row0 < rows, or
+                       // the tile holds none)
+};
+__device__ __forceinline__ RowTile row_tile(const AttnArgs& a, int64_t tile, int G, int per) {
+  int b = 0;  // the last b with first_tile(b) <= tile
+  for (int lo = 0, hi = a.B; lo < hi;) {
+    const int mid = (lo + hi) / 2;
+    if (first_tile(a, mid, G, per) <= tile) {
+      b = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid;
+    }
+  }
+  const int t0 = min(max(a.tok_indptr[b], 0), a.R);
+  const int t1 = min(max(a.tok_indptr[b + 1], 0), a.R);
+  return {b, t0, (tile - first_tile(a, b, G, per)) * per, (int64_t)(t1 - t0) * G};
 }
 
 }  // namespace idxk

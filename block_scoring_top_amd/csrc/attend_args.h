@@ -25,9 +25,10 @@ struct AttnArgs {
   float softcap;              // 0: none
 };
 
-// Tiles of 64 tokens per workgroup, and workgroups per row.
+// Tiles of 64 tokens per workgroup, and workgroups per row; rows of a workgroup where
+// packed tokens share one.
 struct AttnSplit {
-  int chunk, splits;
+  int chunk, splits, rows;
 };
 
 }  // namespace idxk

@@ -236,7 +236,7 @@ int idx_attend_prefill(const void* q, int64_t q_stride, const uint8_t* k_cache,
   const idxk::AttnSplit sp =
       idxk::attend_prefill_split(n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size));
   if ((int64_t)n_tok * Hq * sp.splits > kMaxInt ||
-      idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv) * Hkv * sp.splits > kMaxInt)
+      idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits > kMaxInt)
     return IDX_ERR_INVALID_ARG;
   const int wst = check_workspace(ws, ws_bytes, partial_bytes(n_tok, Hq, sp.splits));
   if (wst != IDX_OK) return wst;

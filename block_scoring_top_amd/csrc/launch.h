@@ -90,7 +90,7 @@ int launch_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v
 // (idx_attend, idx_attend_prefill); splits > 1 needs part_o and part_ml.
 AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units);
 AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units);
-int64_t attend_prefill_tiles(int64_t n_tok, int B, int G);  // workgroups per head and split
+int64_t attend_prefill_tiles(int64_t n_tok, int B, int G, int per);  // of `per` rows
 int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend_merge(const AttnArgs& a, int splits, void* stream);

@@ -164,6 +164,8 @@ int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const ui
  * [0, n_tok]; entries outside that range are clamped to it.
  *   q, out [n_tok, Hq, D]; kv_len [n_tok]; the other arguments, the limits and
  *   the arithmetic are those of idx_attend. B <= IDX_MAX_REQUESTS.
+ * Calls of few rows a request (n_tok * Hq / Hkv / B up to 64: drafted tokens) share out
+ * the keys among waves, longer prompts the rows; a batch of both does best as two calls.
  */
 size_t idx_attend_prefill_workspace_bytes(int n_tok, int B, int Hq, int Hkv, int max_pages,
                                           int page_size);

@@ -481,6 +481,28 @@ def test_prefill_leaves_other_rows_as_they_were():
     check_rows(out, c, q64, [0] * 2 + [1] * (n + 5), [5] * (n + 7))
 
 
+def test_prefill_few_rows_with_nan_values_prefixes_and_empty_rows():
+    """The same in calls of few rows a request: drafted tokens on longer contexts."""
+    lens, news = [200, 77, 1000, 5, 64, 300], [6, 5, 7, 5, 1, 0]
+    c = Cache(54, lens, 2, 16)
+    for b, pos, dim in ((0, 197, 3), (0, 10, 100), (2, 995, 127), (3, 2, 64), (4, 63, 0)):
+        page = c.indices[c.indptr[b] + pos // 16]
+        c.v[page, 1, dim, pos % 16] = 0x7F if dim % 2 else 0xFF
+    c.k[c.indices[c.indptr[1] + 74 // 16], 0, 74 % 16, 5] = 0x7F
+    ptr, req, seen = causal(lens, news)
+    seen[7], seen[12], seen[19] = 77, 0, -3       # a prefix's row, rows that see nothing
+    for Hq in (2, 6, 16, 32):
+        q, q64 = queries(c.rng, len(req), Hq)
+        assert len(req) * (Hq // 2) <= 64 * len(lens)
+        for kw in ({}, dict(softcap=20.0), dict(slopes=dev(np.full(Hq, 0.05, np.float32)))):
+            out = prefill(c, q, ptr, seen, **kw)
+            check_rows(out, c, q64, req, seen, cap=kw.get("softcap", 0.0),
+                       slopes=np.full(Hq, np.float32(0.05)) if "slopes" in kw else None)
+            nan = out.isnan().cpu().numpy()
+            assert nan[:6, Hq // 2:, 100].all() and not nan[:3, :, 3].any()
+            assert nan[3:6, Hq // 2:, 3].all() and not nan[12].any() and not nan[19].any()
+
+
 def test_prefill_nan_values_reach_only_the_rows_that_see_them():
     lens = [140, 140]
     c = Cache(46, lens, 2, 16)
