@@ -64,7 +64,8 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   RowTile rt{0, r, 16 * NT * band, G};
   bool known = true;
   if constexpr (PACKED) {
-    rt = row_tile(a, r, G, 16 * NT);
+    __shared__ int found;
+    rt = row_tile<kAtNT>(a, r, G, 16 * NT, &found);
     if (rt.row0 < 0 || rt.row0 >= rt.rows) return;
   } else {
     rt.b = a.row_req == nullptr ? r : a.row_req[r];

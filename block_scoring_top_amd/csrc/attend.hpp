@@ -346,17 +346,18 @@ struct RowTile {
   int64_t row0, rows;  // first row of the tile, rows of the request (0 <= row0 < rows, or
                        // the tile holds none)
 };
-__device__ __forceinline__ RowTile row_tile(const AttnArgs& a, int64_t tile, int G, int per) {
-  int b = 0;  // the last b with first_tile(b) <= tile
-  for (int lo = 0, hi = a.B; lo < hi;) {
-    const int mid = (lo + hi) / 2;
-    if (first_tile(a, mid, G, per) <= tile) {
-      b = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid;
-    }
-  }
+// (Every request is looked at by a thread of the workgroup at once: a search by halves is
+// a chain of loads, 77.5 us against 75.9 for 47 short prompts.) found: a word of LDS.
+template <int NT>
+__device__ __forceinline__ RowTile row_tile(const AttnArgs& a, int64_t tile, int G, int per,
+                                            int* found) {
+  if (threadIdx.x == 0) *found = -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.B; i += NT)
+    if (first_tile(a, i, G, per) <= tile && tile < first_tile(a, i + 1, G, per)) *found = i;
+  __syncthreads();
+  const int b = *found;
+  if (b < 0) return {0, 0, 0, 0};
   const int t0 = min(max(a.tok_indptr[b], 0), a.R);
   const int t1 = min(max(a.tok_indptr[b + 1], 0), a.R);
   return {b, t0, (tile - first_tile(a, b, G, per)) * per, (int64_t)(t1 - t0) * G};

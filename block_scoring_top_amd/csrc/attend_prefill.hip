@@ -58,7 +58,8 @@ struct PreLds {
   // NaN value codes of a tile that some rows see only in part: which tile (plus one),
   // and for each dim and unit which of its 16 tokens
   int nan_tile[2];
-  uint16_t nan_map[2][kHeadDim][4];
+  alignas(8) uint16_t nan_map[2][kHeadDim][4];
+  int found;
 };
 
 __device__ __forceinline__ float halves_max(float v) {
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   const int G = a.Hq / a.Hkv;
   const int ush = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(units a page)
 
-  const RowTile rt = row_tile(a, tile, G, kPreRows);
+  const RowTile rt = row_tile<kPreNT>(a, tile, G, kPreRows, &lds.found);
   const int t0 = rt.t0;
   const int64_t row0 = rt.row0, rows = rt.rows;
   if (row0 < 0 || row0 >= rows) return;

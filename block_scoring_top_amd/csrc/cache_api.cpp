@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of a launch
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -157,7 +158,8 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
   if (dt != IDX_F32 && dt != IDX_BF16) return IDX_ERR_INVALID_ARG;
   if (D != IDX_HEAD_DIM || !page_size_built(page_size)) return IDX_ERR_UNSUPPORTED;
   if ((int64_t)n_pages * Hkv > kMaxInt || (int64_t)n_pages * page_size > kMaxInt ||
-      (int64_t)n_tok * Hkv > kMaxInt || (int64_t)Hkv * D > kMaxInt || n_tok > 1 << 30)
+      (int64_t)n_tok * Hkv > kMaxInt || (int64_t)Hkv * D > kMaxInt ||
+      n_tok > 1 << 30 || ((int64_t)n_tok / 16 + 1) * ((Hkv + 1) / 2) * 256 > kMaxThreads)
     return IDX_ERR_INVALID_ARG;
   if (n_tok > 0) {
     if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr ||
@@ -199,7 +201,11 @@ int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const ui
   if (R == 0) return IDX_OK;
   const idxk::AttnSplit sp =
       idxk::attend_rows_split(R, Hkv, row_units(max_pages, K, page_size));
-  if ((int64_t)R * Hq * sp.splits > kMaxInt) return IDX_ERR_INVALID_ARG;
+  // (256 threads for each of at most two workgroups a row, KV head and split; the join
+  // takes a wave for two query heads of a row)
+  if ((int64_t)R * Hkv * sp.splits * (Hq / Hkv > 32 ? 2 : 1) * 256 > kMaxThreads ||
+      (int64_t)R * Hq * 64 > kMaxThreads || (int64_t)R * Hq * sp.splits > kMaxInt)
+    return IDX_ERR_INVALID_ARG;
   const int wst = check_workspace(ws, ws_bytes, partial_bytes(R, Hq, sp.splits));
   if (wst != IDX_OK) return wst;
   idxk::AttnArgs a = attend_args(q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
@@ -236,7 +242,9 @@ int idx_attend_prefill(const void* q, int64_t q_stride, const uint8_t* k_cache,
   const idxk::AttnSplit sp =
       idxk::attend_prefill_split(n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size));
   if ((int64_t)n_tok * Hq * sp.splits > kMaxInt ||
-      idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits > kMaxInt)
+      (int64_t)n_tok * Hq * 64 > kMaxThreads ||
+      idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits * 512 >
+          kMaxThreads)
     return IDX_ERR_INVALID_ARG;
   const int wst = check_workspace(ws, ws_bytes, partial_bytes(n_tok, Hq, sp.splits));
   if (wst != IDX_OK) return wst;

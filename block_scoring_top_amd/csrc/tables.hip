@@ -109,7 +109,7 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(
     have[i] = b < B ? min(max(seq_len[b], 0), most) : 0;
     change[i] = b < B ? n_new[b] : 0;
   }
-  const int head = ((cursor[0] % n_pages) + n_pages) % n_pages;
+  const int turn = cursor[0] % n_pages, head = turn < 0 ? turn + n_pages : turn;
   const int free_n = min(max(cursor[1], 0), n_pages);
   // division by page_size, a shift where it is a power of two
   auto div = [&](uint32_t x) {

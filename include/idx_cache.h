@@ -139,8 +139,10 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * value, whose e4m3 code is exact there. That holds while the value scales of
  * one head that matter lie within 2^20 of each other.
  * scale finite, and the scores finite in fp32; softcap 0 (none) or from
- * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued),
+ * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued), B >= 1,
  * 1 <= Hq / Hkv <= IDX_MAX_GROUP, Hq a multiple of Hkv, page_size 16, 32 or 64.
+ * Calls whose launch would pass 2^32 - 1 threads (R * Hkv from about 2^23 on) are
+ * refused (IDX_ERR_INVALID_ARG).
  * max_pages may be any bound of the lists' lengths; how rows are cut for the chip goes
  * by it, so that work spreads best when it is near the longest list.
  * ws: at least idx_attend_workspace_bytes(...) bytes (256-byte aligned; may be

@@ -55,6 +55,7 @@ WRITE = dict(k=P, v=P, k_stride=512, v_stride=512, slots=P, k_cache=P, v_cache=P
     (dict(n_tok=-1), INVALID), (dict(Hkv=0), INVALID), (dict(n_pages=0), INVALID),
     (dict(page_size=0), INVALID), (dict(dt=2), INVALID), (dict(n_pages=1 << 30), INVALID),
     (dict(n_tok=(1 << 30) + 1, Hkv=1), INVALID),
+    (dict(n_tok=1 << 26, Hkv=32, k_stride=4096, v_stride=4096), INVALID),
     (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED),
     (dict(page_size=128), UNSUPPORTED), (dict(D=64), UNSUPPORTED),
     (dict(n_tok=0), OK), (dict(n_tok=0, k=None, slots=None), OK),
@@ -89,6 +90,7 @@ SHARED = [
     (dict(R=-1), INVALID), (dict(R=3), INVALID), (dict(row_req=P + 2), INVALID),
     (dict(ids=P, K=0), INVALID), (dict(K=4), INVALID), (dict(ids=P + 1, K=4), INVALID),
     (dict(ids=P, K=-1), INVALID), (dict(max_pages=4096), WORKSPACE),
+    (dict(R=1 << 22, row_req=P), INVALID), (dict(R=1 << 26, Hq=1, Hkv=1, q_stride=128, row_req=P), INVALID),
     (dict(max_pages=4096, ws=P + 16, ws_bytes=1 << 30), WORKSPACE), (dict(R=0), OK),
     (dict(R=0, q=None, out=None), OK),
 ])
@@ -103,6 +105,7 @@ PRE = (dict(list(PRE.items())[:8]) | dict(tok_indptr=P, kv_len=P, slopes=None, o
 
 @pytest.mark.parametrize("kw,want", SHARED + [
     (dict(n_tok=-1), INVALID), (dict(tok_indptr=None), INVALID), (dict(tok_indptr=P + 2), INVALID),
+    (dict(n_tok=1 << 30), INVALID),
     (dict(B=16385), UNSUPPORTED), (dict(max_pages=4096), WORKSPACE),
     (dict(max_pages=4096, ws=P + 16, ws_bytes=1 << 30), WORKSPACE), (dict(n_tok=0), OK),
 ])
