@@ -262,7 +262,7 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
         top = fmaxf(top, y);
       }
     // uncapped scores are scaled by ksc > 0 from here on (not 0, for masked ones)
-    const float sc = KIND != kPlain ? 1.f : fmaxf(ksc, 1e-30f);
+    const float sc = KIND != kPlain ? 1.f : fmaxf(ksc, 0x1p-126f);
     top = groups_max(top * sc);
     if (__any(top > st.m[j] + kLazy)) {
       const float m = fmaxf(st.m[j], top);

@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 #pragma unroll
       for (int ts = 0; ts < 2; ++ts) {
         // not 0, which would make NaN of the masked scores of a unit without tokens
-        ksc[ts] = fmaxf(ksc[ts], 1e-30f);
+        ksc[ts] = fmaxf(ksc[ts], 0x1p-126f);
         float mx = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < 16; ++j) {

@@ -138,7 +138,8 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * bf16 products; a probability is rounded to 11 bits (fp16) before it meets its
  * value, whose e4m3 code is exact there. That holds while the value scales of
  * one head that matter lie within 2^20 of each other.
- * scale finite, and the scores finite in fp32; softcap 0 (none) or from
+ * scale finite, |q| at most 2^104 (products of queries and codes are summed before the
+ * key scale meets them) and the scores finite in fp32; softcap 0 (none) or from
  * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued), B >= 1,
  * 1 <= Hq / Hkv <= IDX_MAX_GROUP, Hq a multiple of Hkv, page_size 16, 32 or 64.
  * Calls whose launch would pass 2^32 - 1 threads (R * Hkv from about 2^23 on) are

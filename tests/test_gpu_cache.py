@@ -588,6 +588,23 @@ def test_value_scales_that_grow_along_the_row():
     check_rows(attend(c, q, seen, row_req=i32(req)), c, q64, req, seen)
 
 
+def test_least_key_scales_under_large_queries():
+    """Keys of very small scale with queries that make ordinary scores of them, in tiles
+    that are masked in part."""
+    lens, news = [300, 77, 20], [40, 77, 1]
+    c = Cache(53, lens, 2, 16)
+    used = c.indices
+    c.ks[used] *= np.float32(2.0 ** -100)
+    ptr, req, seen = causal(lens, news)
+    q, _ = queries(c.rng, len(req), 6)
+    q = (q.float() * 2.0 ** 100).bfloat16()
+    q64 = q.double().numpy()
+    check_rows(attend(c, q, seen, row_req=i32(req)), c, q64, req, seen)
+    check_rows(prefill(c, q, ptr, seen), c, q64, req, seen)
+    few = ptr[:3]                                         # a row of each request
+    check_rows(prefill(c, q[few], [0, 1, 2, 3], seen[few]), c, q64[few], req[few], seen[few])
+
+
 def test_rows_and_prompt_tokens_agree():
     """The same rows through both calls: equal within both bounds of the oracle."""
     lens, news = [700, 90, 1300], [5, 1, 3]
