@@ -407,15 +407,19 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
   if (row >= rows) return;
   // lane: dims 32 dt + 8 q + 4 half + e of its row
   if (splits == 1) {
-    const float inv = l == 0.f ? 0.f : vref / l;
+    // (vref / l would lose its bits below fp32's normal range)
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* out = a.out + (tok * a.Hq + hq) * kHeadDim;
 #pragma unroll
     for (int dt = 0; dt < 4; ++dt)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int g = 0; g < 4; ++g) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = o[dt][4 * g + e] * inv * vref;
         *reinterpret_cast<uint2*>(out + 32 * dt + 8 * g + 4 * half) =
-            make_uint2(pack_bf16(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv),
-                       pack_bf16(o[dt][4 * g + 2] * inv, o[dt][4 * g + 3] * inv));
+            make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      }
   } else {
     const int64_t part = (((tok * a.Hkv + h) * splits) + split) * G + hq % G;
     float* out = a.part_o + part * kHeadDim;

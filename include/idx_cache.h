@@ -137,7 +137,8 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * Scores, softmax statistics and sums are fp32; keys and queries meet as exact
  * bf16 products; a probability is rounded to 11 bits (fp16) before it meets its
  * value, whose e4m3 code is exact there. That holds while the value scales of
- * one head that matter lie within 2^20 of each other.
+ * one head that matter lie within 2^20 of each other, and none above 2^70 (sums are
+ * kept in units of the largest).
  * scale finite, |q| at most 2^104 (products of queries and codes are summed before the
  * key scale meets them) and the scores finite in fp32; softcap 0 (none) or from
  * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued), B >= 1,

@@ -605,6 +605,26 @@ def test_least_key_scales_under_large_queries():
     check_rows(prefill(c, q[few], [0, 1, 2, 3], seen[few]), c, q64[few], req[few], seen[few])
 
 
+def test_least_value_scales_in_long_uncut_prompts():
+    """Values of the least scale under a large sum of weights: 64 tokens of score 0, the
+    others below the step at which the reference moves (5.5 in base 2)."""
+    n, Hkv = 2000, 8
+    c = Cache(54, [n], Hkv, 16)
+    c.k[c.indices] = 0x38                                 # 1.0
+    c.k[c.indices[:4]] = 0
+    c.ks[c.indices] = 2.0 ** -7
+    c.vs[c.indices] = 2.0 ** -120
+    c.poison_tails()
+    q = torch.ones(1000, 64, 128, dtype=torch.bfloat16)
+    ptr, req, seen = causal([n], [1000])
+    # enough row tiles that no row is cut: there are no partial results
+    assert idx.idx_attend_prefill_workspace_bytes(1000, 1, 64, Hkv, c.max_pages, 16) == 0
+    scale = 5.5 * np.log(2.0)                             # times the product, 128 * 2^-7
+    rows = [0, 500, 999]
+    out = prefill(c, q, ptr, seen, scale=scale)
+    check_rows(out, c, q.double().numpy(), req, seen, scale=scale, rows=rows)
+
+
 def test_rows_and_prompt_tokens_agree():
     """The same rows through both calls: equal within both bounds of the oracle."""
     lens, news = [700, 90, 1300], [5, 1, 3]
