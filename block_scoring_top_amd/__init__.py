@@ -573,9 +573,11 @@ def _scratch(nbytes, ws, dev):
 def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages,
                row_req=None, ids=None, scale=None, softcap=0.0, slopes=None, out=None, ws=None):
     """Attention of single tokens q [R, Hq, 128] (bf16) over the paged 8-bit cache: row r
-    sees the first kv_len[r] tokens of request row_req[r] (of request r without it), all
-    of them or, with ids [R, K], those of the selected page slots (-1: none), as
-    idx_select_paged returns them. softcap: scores become softcap * tanh(x / softcap);
+    sees the first kv_len[r] tokens of request row_req[r] (of request r without it, which
+    the packed rows of PageTables are only while every request adds exactly one token: give
+    row_req=tok_req with tok_len), all of them or, with ids [R, K], those of the selected
+    page slots (-1: none), a line for each row; idx_select_paged returns one for each
+    request, so ids[tok_req] for packed rows. softcap: scores become softcap * tanh(x / softcap);
     slopes [Hq]: minus slope * distance. Returns out [R, Hq, 128]; a row that sees
     nothing is zero."""
     lib = _lib or load()

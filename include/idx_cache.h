@@ -130,7 +130,8 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  *   q   [R, Hq, D] bf16, 16-byte aligned, rows q_stride elements apart (a
  *       multiple of 8, at least Hq * D)
  *   out [R, Hq, D] bf16, dense, 16-byte aligned
- *   kv_len [R]; row_req [R] or NULL (row r is request r; then R <= B)
+ *   kv_len [R]; row_req [R] or NULL (row r is request r; then R <= B): for rows as
+ *       idx_page_tables packs them, tok_len and tok_req
  *   ids [R, K] or NULL (then K is 0); slopes [Hq] float32 or NULL
  * A prefix mask (tokens of a prefix see all of it) needs no argument: give each
  * row of the prefix the prefix's length as kv_len.
