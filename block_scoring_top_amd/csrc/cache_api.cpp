@@ -201,10 +201,9 @@ int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const ui
   if (R == 0) return IDX_OK;
   const idxk::AttnSplit sp =
       idxk::attend_rows_split(R, Hkv, row_units(max_pages, K, page_size));
-  // (256 threads for each of at most two workgroups a row, KV head and split; the join
-  // takes a wave for two query heads of a row)
-  if ((int64_t)R * Hkv * sp.splits * (Hq / Hkv > 32 ? 2 : 1) * 256 > kMaxThreads ||
-      (int64_t)R * Hq * 64 > kMaxThreads || (int64_t)R * Hq * sp.splits > kMaxInt)
+  // 256 threads for each of at most two workgroups a row, KV head and split (rows are cut,
+  // and joined, only where rows times KV heads are a few hundred)
+  if ((int64_t)R * Hkv * sp.splits * (Hq / Hkv > 32 ? 2 : 1) * 256 > kMaxThreads)
     return IDX_ERR_INVALID_ARG;
   const int wst = check_workspace(ws, ws_bytes, partial_bytes(R, Hq, sp.splits));
   if (wst != IDX_OK) return wst;
@@ -241,10 +240,9 @@ int idx_attend_prefill(const void* q, int64_t q_stride, const uint8_t* k_cache,
   if (n_tok == 0) return IDX_OK;
   const idxk::AttnSplit sp =
       idxk::attend_prefill_split(n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size));
-  if ((int64_t)n_tok * Hq * sp.splits > kMaxInt ||
-      (int64_t)n_tok * Hq * 64 > kMaxThreads ||
-      idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits * 512 >
-          kMaxThreads)
+  // up to 512 threads for each row tile, KV head and split
+  if (idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits * 512 >
+      kMaxThreads)
     return IDX_ERR_INVALID_ARG;
   const int wst = check_workspace(ws, ws_bytes, partial_bytes(n_tok, Hq, sp.splits));
   if (wst != IDX_OK) return wst;

@@ -144,8 +144,8 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * key scale meets them) and the scores finite in fp32; softcap 0 (none) or from
  * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued), B >= 1,
  * 1 <= Hq / Hkv <= IDX_MAX_GROUP, Hq a multiple of Hkv, page_size 16, 32 or 64.
- * Calls whose launch would pass 2^32 - 1 threads (R * Hkv from about 2^23 on) are
- * refused (IDX_ERR_INVALID_ARG).
+ * Calls whose launch would pass 2^32 - 1 threads are refused (IDX_ERR_INVALID_ARG): R * Hkv
+ * from 2^24 on, from 2^23 on for groups above 32 heads.
  * max_pages may be any bound of the lists' lengths; how rows are cut for the chip goes
  * by it, so that work spreads best when it is near the longest list.
  * ws: at least idx_attend_workspace_bytes(...) bytes (256-byte aligned; may be
@@ -168,7 +168,10 @@ int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const ui
  * (past tok_indptr[B]) keep their output. tok_indptr is ascending within
  * [0, n_tok]; entries outside that range are clamped to it.
  *   q, out [n_tok, Hq, D]; kv_len [n_tok]; the other arguments, the limits and
- *   the arithmetic are those of idx_attend. B <= IDX_MAX_REQUESTS.
+ *   the arithmetic are those of idx_attend. B <= IDX_MAX_REQUESTS. The launch is taken at 512
+ *   threads for each KV head and tile of 256 rows (token, head of the group), of 16 rows in
+ *   calls of few rows a request: refused where n_tok * Hq + 256 * B * Hkv reaches 2^31, or a
+ *   sixteenth of that.
  * Calls of few rows a request (n_tok * Hq / Hkv / B up to 64: drafted tokens) share out
  * the keys among waves, longer prompts the rows; a batch of both does best as two calls.
  */
