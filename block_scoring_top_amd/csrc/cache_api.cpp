@@ -158,8 +158,8 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
   if (dt != IDX_F32 && dt != IDX_BF16) return IDX_ERR_INVALID_ARG;
   if (D != IDX_HEAD_DIM || !page_size_built(page_size)) return IDX_ERR_UNSUPPORTED;
   if ((int64_t)n_pages * Hkv > kMaxInt || (int64_t)n_pages * page_size > kMaxInt ||
-      (int64_t)n_tok * Hkv > kMaxInt || (int64_t)Hkv * D > kMaxInt ||
-      n_tok > 1 << 30 || ((int64_t)n_tok / 16 + 1) * ((Hkv + 1) / 2) * 256 > kMaxThreads)
+      (int64_t)Hkv * D > kMaxInt ||
+      ((int64_t)n_tok / 16 + 1) * (((int64_t)Hkv + 1) / 2) * 256 > kMaxThreads)
     return IDX_ERR_INVALID_ARG;
   if (n_tok > 0) {
     if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr ||

@@ -103,8 +103,8 @@ int idx_page_tables(const int32_t* seq_len, const int32_t* n_new, const int32_t*
  *          and the tokens of one page lie in consecutive rows, in order of
  *          their offsets and without gaps; otherwise that page's contents are
  *          unspecified.
- * 0 <= n_tok <= 2^30 (0: nothing is enqueued), dt IDX_F32 or IDX_BF16, page_size 16, 32
- * or 64.
+ * n_tok >= 0 (0: nothing is enqueued) and n_tok * ceil(Hkv / 2) below 2^28 (the launch; larger
+ * calls are refused, IDX_ERR_INVALID_ARG), dt IDX_F32 or IDX_BF16, page_size 16, 32 or 64.
  */
 int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                     const int32_t* slots, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,

@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 import block_scoring_top_amd as idx
 from tests.cache_helpers import Cache, check_rows, queries
 from tests.test_abi import HIPERR, INVALID, P
-from tests.test_cache_abi import PRE, ROWS
+from tests.test_cache_abi import PRE, ROWS, WRITE
 
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would run")
 
@@ -46,6 +46,24 @@ def test_prompt_tokens_up_to_the_launch(lib, n, Hq, Hkv, B, want):
     assert lib.idx_attend_prefill_workspace_bytes(n, B, Hq, Hkv, 2, 16) == 0
     args = PRE | sized(n, Hq, Hkv, n_tok=n, B=B)
     assert lib.idx_attend_prefill(*args.values(), None) == want
+
+
+# 256 threads for 16 rows and 2 KV heads: n_tok * ceil(Hkv / 2) below 2^28, as documented
+@no_gpu
+@pytest.mark.parametrize("n,Hkv,want", [
+    ((1 << 28) - 17, 1, HIPERR), ((1 << 28) - 17, 2, HIPERR), (1 << 28, 1, INVALID),
+    ((1 << 26) - 17, 8, HIPERR), (1 << 26, 8, INVALID), ((1 << 31) - 1, 1, INVALID)])
+def test_written_tokens_up_to_the_launch(lib, n, Hkv, want):
+    stride = 128 * Hkv
+    args = WRITE | dict(n_tok=n, Hkv=Hkv, k_stride=stride, v_stride=stride)
+    assert lib.idx_cache_write(*args.values(), None) == want
+
+
+def test_the_header_states_the_bound_of_written_tokens():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "idx_cache.h")) as f:
+        text = f.read()
+    assert "n_tok <= 2^30" not in text and "n_tok * ceil(Hkv / 2)" in text
 
 
 @pytest.mark.gpu
