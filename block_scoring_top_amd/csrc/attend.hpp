@@ -15,7 +15,9 @@
 // the row's maximum has grown by kLazy or more (most tiles then leave the sums alone): it
 // reaches 2^(kPBias + kLazy), which fp16 holds, and keeps 11 bits down to 2^-23 of the
 // row's largest. The value scale of a unit enters with the exponential's argument, as a
-// logarithm relative to the largest scale met, and leaves the sum of weights once a unit.
+// logarithm relative to the largest scale that the row has seen, and leaves the sum of
+// weights once a unit. References are each row's own: rows that share products see
+// different tokens, and no bit of one depends on what only another sees.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -108,7 +110,9 @@ template <int NT>
 struct AttnState {
   at_f32x4 o[NT][8];  // dims 16 dt + 4 g + i of query row n
   float m[NT], l[NT];  // m: all groups alike; l: this group's units alone
-  float vref, lref;    // largest value scale met, and its logarithm: o is in its units
+  // largest value scale seen, and its logarithm: o is in its units (rows of different
+  // visible lengths: each lane's row has its own, and NT is 1)
+  float vref, lref;
 };
 
 template <int NT>
@@ -209,12 +213,14 @@ __device__ __forceinline__ void attn_nan_values(AttnState<NT>& st, uint4 (&v)[8]
 // ksc: the score scale of unit g; vs: its value scale, 0 if it holds no token; pos:
 // position of its first token; have: how many of its tokens exist; len: visible length
 // of each of the lane's query rows; any: whether a token of the tile is masked for any
-// row (uniform over the wave). MIXED: the rows' visible lengths differ.
+// row (uniform over the wave). MIXED: the rows' visible lengths differ (then NT is 1).
 template <int NT, int KIND, bool MIXED>
 __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q)[NT][4],
                                           const uint4 (&k)[4][2], uint4 (&v)[8], float ksc,
                                           float vs, int pos, int have, const int (&len)[NT],
                                           const float (&slope2)[NT], const Cap& cap, bool any) {
+  static_assert(!MIXED || NT == 1, "one reference of the value scales a lane");
+  if (MIXED && pos >= len[0]) vs = 0.f;  // none of the unit for this row
   const float vtop = groups_max(vs);
   if (vtop > st.vref) {
     const float f = st.vref / vtop;
@@ -265,7 +271,7 @@ __device__ __forceinline__ void attn_tile(AttnState<NT>& st, const at_bf16x8 (&q
     const float sc = KIND != kPlain ? 1.f : fmaxf(ksc, 0x1p-126f);
     top = groups_max(top * sc);
     if (__any(top > st.m[j] + kLazy)) {
-      const float m = fmaxf(st.m[j], top);
+      const float m = top > st.m[j] + kLazy ? top : st.m[j];
       const float f = exp2_fast(st.m[j] - (m == -__builtin_inff() ? 0.f : m));
       st.m[j] = m;
       st.l[j] *= f;

@@ -44,6 +44,7 @@ constexpr int kPackedMean = 64;               // rows a request, up to which the
 constexpr int kCUs = 256;
 constexpr int kPhase = 512;                   // tiles whose page data wait in LDS
 constexpr int kPreUnits = 4 * (kPhase + 4);   // and for the tiles loaded ahead
+static_assert(kPhase <= kPreNT, "a thread for each tile of a phase");
 constexpr int kAhead = 4;                     // operands read from LDS before their use
 constexpr int kFrag = kWave;                  // uint4s of one operand in LDS
 
@@ -52,6 +53,7 @@ struct PreLds {
   uint4 v[2][16][kFrag];  // [buffer][32-dim tile, 32-token half, 8 tokens of the units]
   int u_blk[kPreUnits];
   float u_ks[kPreUnits], u_lv[kPreUnits];
+  float u_vmax[4 * kPhase];  // largest value scale of the phase's units up to each
   float red[kPreWaves];
   int longest[kPreWaves], shortest[kPreWaves];
   unsigned long long work[kPreWaves];
@@ -217,7 +219,9 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m = -__builtin_inff(), l = 0.f;
-  float vref = 0.f;     // the largest value scale so far: o is in its units
+  // the largest value scale of the units the row sees, up to the phase's end, and its
+  // logarithm: o is in its units
+  float vref = 0.f, lref = 0.f;
   float ksc[2], lv[2];  // scales of the tile
 
   // operands are read from LDS kAhead products before their use
@@ -252,7 +256,8 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     for (int ts = 0; ts < 2; ++ts) {
       const int i = 4 * c + 2 * ts + half, pos = (4 * begin + i) * kUnit;
       ksc[ts] = lds.u_ks[i];
-      lv[ts] = lds.u_lv[i];
+      // (2^-60 below the reference fp16 holds nothing; nor does a unit without tokens)
+      lv[ts] = fmaxf(lds.u_lv[i] - lref, -60.f);
       have[ts] = lds.u_blk[i] < 0 ? 0 : min(kUnit, len - pos);
       if constexpr (KIND != kPlain) {
         const float bias = -slope2 * (float)(len - 1 - pos);
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
     }
     top = halves_max(top);
     if (__any(top > m + kLazy)) {
-      const float mn = fmaxf(m, top);
+      const float mn = top > m + kLazy ? top : m;
       const float f = exp2_fast(m - (mn == -__builtin_inff() ? 0.f : mn));
       m = mn;
       l *= f;
@@ -358,34 +363,49 @@ __global__ __launch_bounds__(kPreNT) void attend_prefill_kernel(AttnArgs a, int 
         (int)min((int64_t)count, ((int64_t)longest + kTileTok - 1) / kTileTok - begin);
     __syncthreads();  // the phase before has been read
     if (tid < 2) lds.nan_tile[tid] = 0;
-    // page data of the tiles, and the largest value scale
-    float vmax = 0.f;
     for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
       const int u = 4 * begin + i;
       const int blk = i < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
       lds.u_blk[i] = blk;
       lds.u_ks[i] = blk < 0 ? 0.f : a.k_scale[blk] * call_scale;
-      const float vs = blk < 0 ? 0.f : a.v_scale[blk];
-      lds.u_lv[i] = vs;
-      vmax = fmaxf(vmax, vs);
+      lds.u_lv[i] = blk < 0 ? 0.f : a.v_scale[blk];
     }
-    vmax = halves_max(vmax);
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) vmax = fmaxf(vmax, __shfl_xor(vmax, d));
-    if (lane == 0) lds.red[w] = vmax;
     __syncthreads();
+    // The largest value scale up to each unit: a thread for each tile, whose four are
+    // joined to those of the threads and waves before.
+    float up[4], before = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPreWaves; ++i) vmax = fmaxf(vmax, lds.red[i]);
+    for (int i = 0; i < 4; ++i) {
+      before = fmaxf(before, tid < count ? lds.u_lv[4 * tid + i] : 0.f);
+      up[i] = before;
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const float left = __shfl_up(before, d);
+      if (lane >= d) before = fmaxf(before, left);
+    }
+    if (lane == kWave - 1) lds.red[w] = before;
+    before = __shfl_up(before, 1);
+    if (lane == 0) before = 0.f;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) before = fmaxf(before, lds.red[i]);
+    if (tid < count) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lds.u_vmax[4 * tid + i] = fmaxf(before, up[i]);
+        lds.u_lv[4 * tid + i] = __log2f(lds.u_lv[4 * tid + i]);  // (no tokens: -infinity)
+      }
+    }
+    __syncthreads();
+    const int64_t seen = min(((int64_t)len + kUnit - 1) / kUnit - 4 * (int64_t)begin,
+                             4 * (int64_t)count);
+    const float vmax = seen > 0 ? lds.u_vmax[seen - 1] : 0.f;
     if (vmax > vref) {
       const float f = vref / vmax;
 #pragma unroll
       for (int dt = 0; dt < 4; ++dt) o[dt] *= f;
       vref = vmax;
-    }
-    // value scales as logarithms relative to it; below 2^-60 fp16 holds nothing of them
-    for (int i = tid; i < 4 * (count + 4); i += kPreNT) {
-      const float vs = lds.u_lv[i];
-      lds.u_lv[i] = vs == vref ? 0.f : fmaxf(__log2f(vs / vref), -60.f);
+      lref = __log2f(vmax);
     }
     load_k(0);
     load_v(0);

@@ -18,7 +18,7 @@
  * each page and head: value = code * scale.
  *   k_cache [n_pages, Hkv, page_size, D]   a token's key is a row
  *   v_cache [n_pages, Hkv, D, page_size]   a token's value is a column
- *   k_scale, v_scale [n_pages, Hkv] float32, positive and finite
+ *   k_scale, v_scale [n_pages, Hkv] float32, finite, at least 2^IDX_CACHE_MIN_EXP
  * n_pages * Hkv <= 2^31 - 1; the caches themselves may be larger than 4 GiB.
  */
 #ifndef IDX_CACHE_H
@@ -33,7 +33,7 @@ extern "C" {
 #define IDX_MAX_GROUP 64         /* Hq / Hkv of the attention calls               */
 #define IDX_MIN_SOFTCAP 0x1p-20f /* smallest and largest cap of scores: a capped    */
 #define IDX_MAX_SOFTCAP 0x1p16f  /* score is off by up to 2^-20 of the cap          */
-#define IDX_CACHE_MIN_EXP (-120) /* idx_cache_write: no scale below 2^-120        */
+#define IDX_CACHE_MIN_EXP (-120) /* idx_cache_write: least scale, 2^-120          */
 
 /*
  * idx_page_tables -- one step of the page allocator, and the lists the other
@@ -137,12 +137,14 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
  * row of the prefix the prefix's length as kv_len.
  * Scores, softmax statistics and sums are fp32; keys and queries meet as exact
  * bf16 products; a probability is rounded to 11 bits (fp16) before it meets its
- * value, whose e4m3 code is exact there. That holds while the value scales of
- * one head that matter lie within 2^20 of each other, and none above 2^70 (sums are
- * kept in units of the largest).
- * scale finite, |q| at most 2^104 (products of queries and codes are summed before the
- * key scale meets them) and the scores finite in fp32; softcap 0 (none) or from
- * IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP. R >= 0 (0: nothing is enqueued), B >= 1,
+ * value, whose e4m3 code is exact there. That holds while the value scales of the tokens that
+ * a row sees lie within 2^20 of each other, and none above 2^70 (a row's sums are kept in
+ * units of the largest it sees). No bit of a row depends on the codes of tokens that it does
+ * not see, nor on the scales of pages that it sees nothing of.
+ * scale finite, its product with any key scale 0 or at least 2^-126 in size; |q| at most
+ * 2^104 (products of queries and codes are summed before the key scale meets them) and the
+ * scores finite in fp32; softcap 0 (none) or from IDX_MIN_SOFTCAP to IDX_MAX_SOFTCAP.
+ * R >= 0 (0: nothing is enqueued), B >= 1,
  * 1 <= Hq / Hkv <= IDX_MAX_GROUP, Hq a multiple of Hkv, page_size 16, 32 or 64.
  * Calls whose launch would pass 2^32 - 1 threads are refused (IDX_ERR_INVALID_ARG): R * Hkv
  * from 2^24 on, from 2^23 on for groups above 32 heads.
