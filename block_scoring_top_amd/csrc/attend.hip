@@ -337,7 +337,8 @@ int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream) {
   hipLaunchKernelGGL((attend_rows_kernel<NT, KIND, PACKED>), grid, blk, 0, s, a, sp.chunk, \
                      sp.splits, bands)
 #define IDX_KINDS(NT, PACKED)                                  \
-  if (a.softcap > 0.f) IDX_ROWS(NT, kCapped, PACKED);          \
+  if (a.softcap > kNearCap) IDX_ROWS(NT, kCappedFar, PACKED);  \
+  else if (a.softcap > 0.f) IDX_ROWS(NT, kCapped, PACKED);     \
   else if (a.slopes != nullptr) IDX_ROWS(NT, kBiased, PACKED); \
   else IDX_ROWS(NT, kPlain, PACKED)
   if (packed) {

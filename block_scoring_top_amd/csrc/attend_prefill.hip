@@ -499,7 +499,8 @@ int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream) {
 #define IDX_PRE(KIND)                                                                         \
   hipLaunchKernelGGL((attend_prefill_kernel<KIND>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
                      tiles)
-  if (a.softcap > 0.f) IDX_PRE(kCapped);
+  if (a.softcap > kNearCap) IDX_PRE(kCappedFar);
+  else if (a.softcap > 0.f) IDX_PRE(kCapped);
   else if (a.slopes != nullptr) IDX_PRE(kBiased);
   else IDX_PRE(kPlain);
 #undef IDX_PRE

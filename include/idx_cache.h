@@ -31,8 +31,8 @@ extern "C" {
 #endif
 
 #define IDX_MAX_GROUP 64         /* Hq / Hkv of the attention calls               */
-#define IDX_MIN_SOFTCAP 0x1p-20f /* smallest and largest cap of scores: a capped    */
-#define IDX_MAX_SOFTCAP 0x1p16f  /* score is off by up to 2^-20 of the cap          */
+#define IDX_MIN_SOFTCAP 0x1p-20f /* smallest and largest cap of scores: a capped score is off */
+#define IDX_MAX_SOFTCAP 0x1p16f  /* by up to 2^-20 of a cap up to 64, 2^-19 of itself above  */
 #define IDX_CACHE_MIN_EXP (-120) /* idx_cache_write: least scale, 2^-120          */
 
 /*
