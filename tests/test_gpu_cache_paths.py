@@ -81,3 +81,39 @@ def test_lengthened_stretches(lens, news, kind):
     rows = sorted({0, 1, 255, 256, news[0] - 1, news[0], n - 1, n // 2, 9, 300, n - 64})
     check_rows(out, c, q64, req, seen, rows=rows)
     assert torch.equal(out, prefill(c, q, ptr, seen))
+
+
+FORMS = {"plain": {}, "biased": dict(slope=0.02), "capped": dict(cap=10.0),
+         "capped_biased": dict(cap=10.0, slope=0.02), "far": dict(cap=500.0),
+         "far_biased": dict(cap=500.0, slope=0.02)}
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (17, 1), (33, 1), (64, 1), (40, 2)])
+def test_places_without_tokens_in_every_kernel(Hq, Hkv, form):
+    """Units without tokens read the pool's first page in their place, whose codes and
+    scales are NaN here: kernels of one and two row tiles, two bands of heads, packed
+    tokens and prompts, every form of the scores."""
+    lens, page = [1, 16, 77, 500, 1300], 16
+    c = Cache(97, lens, Hkv, page)
+    if (c.indices == 0).any():              # the first page is nobody's
+        c.indices[c.indices == 0] = np.setdiff1d(np.arange(1, c.n_pages), c.indices)[0]
+        c.ks[c.indices], c.vs[c.indices] = 0.03, 0.05
+        c.k[c.indices], c.v[c.indices] = c.k[c.indices] & 0x77, c.v[c.indices] & 0x77
+    c.k[0], c.v[0], c.ks[0], c.vs[0] = 0xFF, 0x7F, np.nan, np.nan
+    slope, cap = FORMS[form].get("slope"), FORMS[form].get("cap", 0.0)
+    slopes = None if slope is None else np.full(Hq, slope, np.float32)
+    kw = dict(softcap=cap, slopes=None if slope is None else torch.from_numpy(slopes).cuda())
+    chk = dict(cap=cap, slopes=slopes)
+    q, q64 = queries(c.rng, len(lens), Hq, 3.0)
+    out = idx.idx_attend(q.cuda(), *c.device(), i32(lens), c.max_pages, **kw)
+    check_rows(out, c, q64, range(len(lens)), lens, **chk)
+    ptr = np.arange(len(lens) + 1)          # a row a request: the packed kernel
+    check_rows(prefill(c, q, ptr, lens, **kw), c, q64, range(len(lens)), lens, **chk)
+    news = [1, 16, 77, 300, 90]             # prompts
+    ptr = np.concatenate([[0], np.cumsum(news)])
+    req = np.repeat(np.arange(len(lens)), news)
+    seen = np.concatenate([np.arange(n - k, n) + 1 for n, k in zip(lens, news)])
+    q, q64 = queries(c.rng, len(req), Hq, 3.0)
+    out = prefill(c, q, ptr, seen, **kw)
+    check_rows(out, c, q64, req, seen, rows=range(0, len(req), 29), **chk)
