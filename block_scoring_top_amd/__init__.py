@@ -611,7 +611,8 @@ def idx_attend_prefill(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indi
                        ws=None):
     """idx_attend for packed prompt tokens q [n, Hq, 128]: request b's rows are
     tok_indptr[b]:tok_indptr[b+1], row t sees the first kv_len[t] tokens of its request
-    (PageTables.tok_len: the causal mask). Rows of no request keep their output."""
+    (PageTables.tok_len: the causal mask). Rows of no request keep their output: give out
+    where they matter, a new one holds anything there."""
     lib = _lib or load()
     dev = _gpu(q)
     n_pages, Hkv, page, D = _cache(dev, k_cache, v_cache, k_scale, v_scale)

@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
         ml[i] = *reinterpret_cast<const at_f32x2*>(a.part_ml + 2 * p);
         if (s >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
       }
-      // (a split without tokens leaves its sums unwritten)
+      // (a split without tokens has no weight: its sums, zeros, need not be read)
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
         x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};

@@ -175,7 +175,9 @@ int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const ui
  *   calls of few rows a request: refused where n_tok * Hq + 256 * B * Hkv reaches 2^31, or a
  *   sixteenth of that.
  * Calls of few rows a request (n_tok * Hq / Hkv / B up to 64: drafted tokens) share out
- * the keys among waves, longer prompts the rows; a batch of both does best as two calls.
+ * the keys among waves, longer prompts the rows; a batch of both does best as two calls. B
+ * counts requests without rows too: a prompt among many idle requests runs best in a call
+ * whose lists name the requests that have rows.
  */
 size_t idx_attend_prefill_workspace_bytes(int n_tok, int B, int Hq, int Hkv, int max_pages,
                                           int page_size);
