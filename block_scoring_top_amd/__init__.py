@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function here checks tensor placement and
 layout, passes raw device pointers and the current HIP stream to the C ABI
-(include/idx.h, include/idx_cache.h) and returns the output tensors. All arithmetic runs in the HIP
+(include/idx.h, idx_cache.h, idx_cache4.h, idx_rope.h) and returns the output tensors. All arithmetic runs in the HIP
 kernels; there is no fallback path. PyTorch supplies device memory and streams.
 """
 from __future__ import annotations
@@ -22,7 +22,10 @@ __all__ = ["idx_score", "idx_topk", "idx_topk_bf16", "idx_select", "idx_select_n
            "IdxError",
            "SelectPlan", "plan_for",
            "idx_page_tables", "PageTables", "idx_cache_write", "idx_attend", "idx_attend_prefill",
-           "idx_attend_workspace_bytes", "idx_attend_prefill_workspace_bytes"]
+           "idx_attend_workspace_bytes", "idx_attend_prefill_workspace_bytes",
+           "idx_rope", "idx_rope_table", "idx_rope_turns", "IDX_ROPE_KINDS",
+           "idx_cache4_write", "idx_cache4_read", "idx_attend4", "idx_attend4_prefill",
+           "idx_attend4_workspace_bytes", "idx_attend4_prefill_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libidx.so")
@@ -31,6 +34,8 @@ IDX_F32, IDX_BF16 = 0, 1
 IDX_SORTED = 0x1
 IDX_RADIX8 = 0x2  # four 8-bit radix passes, no linear-bin pass (same results)
 IDX_CHUNK_SHIFT = 8
+IDX_ROPE_ADJACENT, IDX_ROPE_INVERSE = 0x1, 0x2
+IDX_ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "by_turns": 3, "by_index": 4}
 
 _c_int, _c_size, _vp, _u32 = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_uint32
 _SIGS = {
@@ -76,6 +81,21 @@ _SIGS = {
     "idx_floor_empty": (_c_int, [_c_int, _vp]),
     "idx_floor_read": (_c_int, [_vp, _c_size, _vp, _vp, _c_int, _c_int, _vp]),
     "idx_floor_mfma": (_c_int, [_vp, _c_int, _c_int, _vp, _vp]),
+}
+
+# the 4-bit cache's calls take the 8-bit cache's arguments (other scales)
+for _n in ("write", "attend_workspace_bytes", "attend", "attend_prefill_workspace_bytes",
+           "attend_prefill"):
+    _SIGS["idx_cache4_write" if _n == "write" else "idx_" + _n.replace("attend", "attend4")] = (
+        _SIGS["idx_cache_write" if _n == "write" else "idx_" + _n])
+_SIGS |= {
+    "idx_cache4_read": (_c_int, [_vp] * 7 + [ctypes.c_int64, ctypes.c_int64] + [_c_int] * 6
+                        + [_vp]),
+    "idx_rope_turns": (_c_int, [_vp, _c_int, _vp]),
+    "idx_rope_table": (_c_int, [ctypes.c_double, _c_int, _c_int] + [ctypes.c_double] * 4 + [_vp]),
+    "idx_rope": (_c_int, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp, _vp,
+                          ctypes.c_int64, ctypes.c_int64] + [_c_int] * 6
+                 + [ctypes.c_float, _u32, _c_int, _vp]),
 }
 
 _lib = None
@@ -570,19 +590,12 @@ def _scratch(nbytes, ws, dev):
     return ws.data_ptr(), ws.numel(), ws
 
 
-def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages,
-               row_req=None, ids=None, scale=None, softcap=0.0, slopes=None, out=None, ws=None):
-    """Attention of single tokens q [R, Hq, 128] (bf16) over the paged 8-bit cache: row r
-    sees the first kv_len[r] tokens of request row_req[r] (of request r without it, which
-    the packed rows of PageTables are only while every request adds exactly one token: give
-    row_req=tok_req with tok_len), all of them or, with ids [R, K], those of the selected
-    page slots (-1: none), a line for each row; idx_select_paged returns one for each
-    request, so ids[tok_req] for packed rows. softcap: scores become softcap * tanh(x / softcap);
-    slopes [Hq]: minus slope * distance. Returns out [R, Hq, 128]; a row that sees
-    nothing is zero."""
+def _attend(name, cache, workspace, q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+            kv_len, max_pages, row_req, ids, scale, softcap, slopes, out, ws):
+    """idx_attend over the cache that `cache` checks."""
     lib = _lib or load()
     dev = _gpu(q)
-    n_pages, Hkv, page, D = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    n_pages, Hkv, page, D = cache(dev, k_cache, v_cache, k_scale, v_scale)
     _words(dev, kv_indptr, kv_indices, kv_len, row_req, ids)
     stride, out = _attend_inputs(dev, q, kv_len, slopes, out, ws)
     R, Hq, Dq = q.shape
@@ -597,13 +610,51 @@ def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_
         K = ids.shape[1]
         if K == 0:
             return out.zero_()
-    wp, wn, ws = _scratch(idx_attend_workspace_bytes(R, Hq, Hkv, max_pages, K, page), ws, dev)
-    _launch("idx_attend", dev, lib.idx_attend, q.data_ptr(), stride, k_cache.data_ptr(),
+    wp, wn, ws = _scratch(workspace(R, Hq, Hkv, max_pages, K, page), ws, dev)
+    _launch(name, dev, getattr(lib, name), q.data_ptr(), stride, k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kv_indptr.data_ptr(),
             kv_indices.data_ptr(), kv_len.data_ptr(), _ptr(row_req), _ptr(ids), _ptr(slopes),
             out.data_ptr(), R, kv_indptr.numel() - 1, Hq, Hkv, D, n_pages, kv_indices.numel(),
             max_pages, page, K, D ** -0.5 if scale is None else scale, softcap, IDX_BF16, wp, wn)
     return out
+
+
+def _attend_packed(name, cache, workspace, q, k_cache, v_cache, k_scale, v_scale, kv_indptr,
+                   kv_indices, tok_indptr, kv_len, max_pages, scale, softcap, slopes, out, ws):
+    """idx_attend_prefill over the cache that `cache` checks."""
+    lib = _lib or load()
+    dev = _gpu(q)
+    n_pages, Hkv, page, D = cache(dev, k_cache, v_cache, k_scale, v_scale)
+    _words(dev, kv_indptr, kv_indices, tok_indptr, kv_len)
+    stride, out = _attend_inputs(dev, q, kv_len, slopes, out, ws)
+    n, Hq, Dq = q.shape
+    B = kv_indptr.numel() - 1
+    if D != Dq:
+        raise ValueError("q and the cache differ in head dimension")
+    if tok_indptr.numel() != B + 1:
+        raise ValueError("tok_indptr and kv_indptr must both hold B + 1 entries")
+    wp, wn, ws = _scratch(workspace(n, B, Hq, Hkv, max_pages, page), ws, dev)
+    _launch(name, dev, getattr(lib, name), q.data_ptr(), stride, k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kv_indptr.data_ptr(),
+            kv_indices.data_ptr(), tok_indptr.data_ptr(), kv_len.data_ptr(), _ptr(slopes),
+            out.data_ptr(), n, B, Hq, Hkv, D, n_pages, kv_indices.numel(), max_pages, page,
+            D ** -0.5 if scale is None else scale, softcap, IDX_BF16, wp, wn)
+    return out
+
+
+def idx_attend(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages,
+               row_req=None, ids=None, scale=None, softcap=0.0, slopes=None, out=None, ws=None):
+    """Attention of single tokens q [R, Hq, 128] (bf16) over the paged 8-bit cache: row r
+    sees the first kv_len[r] tokens of request row_req[r] (of request r without it, which
+    the packed rows of PageTables are only while every request adds exactly one token: give
+    row_req=tok_req with tok_len), all of them or, with ids [R, K], those of the selected
+    page slots (-1: none), a line for each row; idx_select_paged returns one for each
+    request, so ids[tok_req] for packed rows. softcap: scores become softcap * tanh(x / softcap);
+    slopes [Hq]: minus slope * distance. Returns out [R, Hq, 128]; a row that sees
+    nothing is zero."""
+    return _attend("idx_attend", _cache, idx_attend_workspace_bytes, q, k_cache, v_cache, k_scale,
+                   v_scale, kv_indptr, kv_indices, kv_len, max_pages, row_req, ids, scale, softcap,
+                   slopes, out, ws)
 
 
 def idx_attend_prefill(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, tok_indptr,
@@ -613,26 +664,186 @@ def idx_attend_prefill(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indi
     tok_indptr[b]:tok_indptr[b+1], row t sees the first kv_len[t] tokens of its request
     (PageTables.tok_len: the causal mask). Rows of no request keep their output: give out
     where they matter, a new one holds anything there."""
+    return _attend_packed("idx_attend_prefill", _cache, idx_attend_prefill_workspace_bytes, q,
+                          k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, tok_indptr,
+                          kv_len, max_pages, scale, softcap, slopes, out, ws)
+
+
+# ---- the paged 4-bit cache (include/idx_cache4.h) -------------------------------------------
+
+_BYTE = torch.uint8
+_E2M1 = getattr(torch, "float4_e2m1fn_x2", _BYTE)  # two codes a byte
+_E8M0 = getattr(torch, "float8_e8m0fnu", _BYTE)
+
+
+def _cache4(dev, k_cache, v_cache, k_scale, v_scale):
+    """Checks a 4-bit cache; returns n_pages, Hkv, page_size, D."""
+    for t in (k_cache, v_cache, k_scale, v_scale):
+        if t.device != dev:
+            raise ValueError("all tensors must live on the same GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    if not (k_cache.dtype is v_cache.dtype and k_cache.dtype in (_BYTE, _E2M1)):
+        raise TypeError("the caches must be uint8 (two codes a byte) or float4_e2m1fn_x2")
+    if not (k_scale.dtype is v_scale.dtype and k_scale.dtype in (_BYTE, _E8M0)):
+        raise TypeError("the scales must be uint8 or float8_e8m0fnu")
+    n_pages, Hkv, page, half = k_cache.shape
+    D = 2 * half
+    if v_cache.shape != (n_pages, Hkv, D, page // 2) or page % 2:
+        raise ValueError("v_cache must be [pages, Hkv, D, page_size / 2] beside k_cache "
+                         "[pages, Hkv, page_size, D / 2]")
+    if k_scale.shape != (n_pages, Hkv, page, D // 32) or v_scale.shape != (n_pages, Hkv, D // 32,
+                                                                           page):
+        raise ValueError("the scales must be [pages, Hkv, page_size, D / 32] (keys) and "
+                         "[pages, Hkv, D / 32, page_size] (values)")
+    return n_pages, Hkv, page, D
+
+
+def idx_cache4_write(k, v, slots, k_cache, v_cache, k_scale, v_scale):
+    """Quantises the keys and values k, v [n, Hkv, 128] (float32 or bf16; token rows may
+    lie apart) into their slots of the 4-bit cache: e2m1 codes, a power-of-two scale for
+    each token, head and 32 dims. The slots of a call are distinct; -1 is skipped."""
+    lib = _lib or load()
+    dev = _gpu(k_cache)
+    n_pages, Hkv, page, D = _cache4(dev, k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _rows("k", k, dev), _rows("v", v, dev)
+    _words(dev, slots)
+    n = slots.numel()
+    if not k.shape == v.shape == (n, Hkv, D) or k.dtype is not v.dtype:
+        raise ValueError("k and v must be [slots, Hkv, D] of one dtype")
+    if k.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    _launch("idx_cache4_write", dev, lib.idx_cache4_write, k.data_ptr(), v.data_ptr(), ks, vs,
+            slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), n, Hkv, D, n_pages, page, _dtype_code(k))
+
+
+def idx_cache4_read(slots, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloat16, k_out=None,
+                    v_out=None):
+    """The keys and values [n, Hkv, 128] that the 4-bit cache holds in the given slots, in
+    any order; -1 gives a row of zeros. New tensors of `dtype` (float32 or bf16), or into
+    k_out and v_out, whose token rows may lie apart. Returns (k, v)."""
+    lib = _lib or load()
+    dev = _gpu(k_cache)
+    n_pages, Hkv, page, D = _cache4(dev, k_cache, v_cache, k_scale, v_scale)
+    _words(dev, slots)
+    shape = (slots.numel(), Hkv, D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=dev)
+    ks, vs = _rows("k_out", k_out, dev), _rows("v_out", v_out, dev)
+    if not k_out.shape == v_out.shape == shape or k_out.dtype is not v_out.dtype:
+        raise ValueError("k_out and v_out must be [slots, Hkv, D] of one dtype")
+    if k_out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {k_out.dtype}")
+    _launch("idx_cache4_read", dev, lib.idx_cache4_read, slots.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_out.data_ptr(),
+            v_out.data_ptr(), ks, vs, shape[0], Hkv, D, n_pages, page, _dtype_code(k_out))
+    return k_out, v_out
+
+
+@functools.lru_cache(maxsize=1024)
+def idx_attend4_workspace_bytes(R, Hq, Hkv, max_pages, K=0, page_size=16) -> int:
+    return load().idx_attend4_workspace_bytes(R, Hq, Hkv, max_pages, K, page_size)
+
+
+@functools.lru_cache(maxsize=1024)
+def idx_attend4_prefill_workspace_bytes(n_tok, B, Hq, Hkv, max_pages, page_size=16) -> int:
+    return load().idx_attend4_prefill_workspace_bytes(n_tok, B, Hq, Hkv, max_pages, page_size)
+
+
+def idx_attend4(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages,
+                row_req=None, ids=None, scale=None, softcap=0.0, slopes=None, out=None, ws=None):
+    """idx_attend over the 4-bit cache (the same arguments, with its codes and scales)."""
+    return _attend("idx_attend4", _cache4, idx_attend4_workspace_bytes, q, k_cache, v_cache,
+                   k_scale, v_scale, kv_indptr, kv_indices, kv_len, max_pages, row_req, ids, scale,
+                   softcap, slopes, out, ws)
+
+
+def idx_attend4_prefill(q, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, tok_indptr,
+                        kv_len, max_pages, scale=None, softcap=0.0, slopes=None, out=None,
+                        ws=None):
+    """idx_attend_prefill over the 4-bit cache (the same arguments, with its codes and
+    scales)."""
+    return _attend_packed("idx_attend4_prefill", _cache4, idx_attend4_prefill_workspace_bytes, q,
+                          k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices, tok_indptr,
+                          kv_len, max_pages, scale, softcap, slopes, out, ws)
+
+
+# ---- rotary positions (include/idx_rope.h) --------------------------------------------------
+
+def idx_rope_turns(inv_freq, device="cuda"):
+    """idx_rope's table from frequencies in radians a token (float64, one for each pair):
+    an int64 tensor [pairs] on `device`, made once."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+    if f.dim() != 1:
+        raise ValueError("inv_freq must be one row of frequencies")
+    out = torch.empty(f.numel(), dtype=torch.int64)
+    _check("idx_rope_turns", load().idx_rope_turns(f.data_ptr(), f.numel(), out.data_ptr()))
+    return out.to(device)
+
+
+def idx_rope_table(rot, base=10000.0, kind="plain", stretch=1.0, original=8192.0, lo=1.0, hi=32.0,
+                   device="cuda"):
+    """idx_rope's table for `rot` rotated dims: frequencies base^(-2 i / rot), stretched for
+    contexts `stretch` times the length `original` in one of the ways of IDX_ROPE_KINDS."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even")
+    if kind not in IDX_ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(IDX_ROPE_KINDS)}")
+    out = torch.empty(rot // 2, dtype=torch.int64)
+    _check("idx_rope_table", load().idx_rope_table(base, rot, IDX_ROPE_KINDS[kind], stretch,
+                                                   original, lo, hi, out.data_ptr()))
+    return out.to(device)
+
+
+def _rope_out(name, x, out, dev):
+    """An output of idx_rope (a new one by default), and its row stride."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError(f"{name} must have its input's shape and dtype")
+    return out, _rows(name, out, dev)
+
+
+def idx_rope(q, k, tok_len, turns, first=0, interleaved=False, inverse=False, factor=1.0,
+             q_out=None, k_out=None):
+    """Rotary positions of q [n, Hq, 128] and k [n, Hkv, 128] (float32 or bf16, token rows may
+    lie apart; k may be None): the dims first .. first + rot of each head turn by their
+    token's position tok_len - 1 (PageTables.tok_len; a row of 0 keeps its outputs), rot =
+    2 * len(turns), the table of idx_rope_table or idx_rope_turns. Pairs are halves of the
+    part, or neighbours with `interleaved`; `inverse` turns back (with the same factor: the
+    gradient). Into new tensors, or q_out and k_out, which may be q and k themselves.
+    Returns (q_out, k_out)."""
     lib = _lib or load()
     dev = _gpu(q)
-    n_pages, Hkv, page, D = _cache(dev, k_cache, v_cache, k_scale, v_scale)
-    _words(dev, kv_indptr, kv_indices, tok_indptr, kv_len)
-    stride, out = _attend_inputs(dev, q, kv_len, slopes, out, ws)
-    n, Hq, Dq = q.shape
-    B = kv_indptr.numel() - 1
-    if D != Dq:
-        raise ValueError("q and the cache differ in head dimension")
-    if tok_indptr.numel() != B + 1:
-        raise ValueError("tok_indptr and kv_indptr must both hold B + 1 entries")
-    wp, wn, ws = _scratch(idx_attend_prefill_workspace_bytes(n, B, Hq, Hkv, max_pages, page), ws,
-                          dev)
-    _launch("idx_attend_prefill", dev, lib.idx_attend_prefill, q.data_ptr(), stride,
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            kv_indptr.data_ptr(), kv_indices.data_ptr(), tok_indptr.data_ptr(),
-            kv_len.data_ptr(), _ptr(slopes), out.data_ptr(), n, B, Hq, Hkv, D, n_pages,
-            kv_indices.numel(), max_pages, page, D ** -0.5 if scale is None else scale, softcap,
-            IDX_BF16, wp, wn)
-    return out
+    qs = _rows("q", q, dev)
+    n, Hq, D = q.shape
+    _words(dev, tok_len)
+    if tok_len.numel() != n:
+        raise ValueError("tok_len must hold one entry per row of q")
+    if (turns.device != dev or turns.dtype is not torch.int64 or turns.dim() != 1
+            or not turns.is_contiguous()):
+        raise ValueError("turns must be a row of int64 on q's GPU")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    q_out, qos = _rope_out("q_out", q, q_out, dev)
+    Hkv, ks, kos, kp, kop = 0, 0, 0, None, None
+    if k is not None:
+        ks = _rows("k", k, dev)
+        Hkv = k.shape[1]
+        if k.shape != (n, Hkv, D) or k.dtype is not q.dtype:
+            raise ValueError("k must be [rows of q, Hkv, D] of q's dtype")
+        k_out, kos = _rope_out("k_out", k, k_out, dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    flags = (IDX_ROPE_ADJACENT if interleaved else 0) | (IDX_ROPE_INVERSE if inverse else 0)
+    _launch("idx_rope", dev, lib.idx_rope, q.data_ptr(), kp, qs, ks, tok_len.data_ptr(),
+            turns.data_ptr(), q_out.data_ptr(), kop, qos, kos, n, Hq, Hkv, D, first,
+            2 * turns.numel(), factor, flags, _dtype_code(q))
+    return q_out, k_out
 
 
 def idx_floor_empty(blocks=1):

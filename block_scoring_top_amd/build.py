@@ -23,11 +23,12 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", os.path.join(ROOT, "include")]
 
 HIP_SOURCES = ["indexer.hip", "indexer_radix8.hip", "assign.hip", "prefill.hip", "pool.hip",
-               "floor.hip", "tables.hip", "cache_write.hip", "attend.hip", "attend_prefill.hip"]
+               "floor.hip", "tables.hip", "cache_write.hip", "attend.hip", "attend_prefill.hip",
+               "cache4.hip", "attend4.hip", "rope.hip"]
 # assign.hip's inputs are finite by contract; without NaN semantics its running
 # max compiles to plain 3-input maxes (no per-operand canonicalisation)
 EXTRA_FLAGS = {"assign.hip": ["-fno-honor-nans"]}
-CXX_SOURCES = ["api.cpp", "cache_api.cpp"]
+CXX_SOURCES = ["api.cpp", "cache_api.cpp", "rope_api.cpp"]
 
 
 def _run(cmd):

@@ -10,7 +10,8 @@ struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
   const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;
+  const float *k_scale, *v_scale;  // 8-bit cache
+  const uint8_t *k_exp, *v_exp;    // 4-bit cache: its scales
   const int32_t *kv_indptr, *kv_indices;
   const int32_t* kv_len;
   const int32_t* row_req;     // single tokens: or NULL

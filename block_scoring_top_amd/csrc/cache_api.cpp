@@ -1,10 +1,13 @@
-// C ABI of the paged 8-bit cache (include/idx_cache.h): host-side argument
-// validation, workspace layout and dispatch. As in api.cpp, validation makes no HIP
-// call.
+// C ABI of the paged 8-bit and 4-bit caches (include/idx_cache.h, include/idx_cache4.h):
+// host-side argument validation, workspace layout and dispatch. As in api.cpp, validation
+// makes no HIP call.
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "idx_cache.h"
+#include "idx_cache4.h"
 #include "launch.h"
 
 namespace {
@@ -41,9 +44,11 @@ bool shape_ok(int64_t rows, int B, int Hq, int Hkv, int max_pages, int page_size
          (int64_t)max_pages * page_size <= kMaxInt;
 }
 
-// What both attention calls check; the workspace and the rows' own arrays apart.
+// What the attention calls check; the workspace and the rows' own arrays apart. Scales are
+// aligned to `scale_align` bytes.
 int check_attend(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
-                 const float* k_scale, const float* v_scale, const int32_t* kv_indptr,
+                 const void* k_scale, const void* v_scale, int scale_align,
+                 const int32_t* kv_indptr,
                  const int32_t* kv_indices, const int32_t* kv_len, const float* slopes,
                  const void* out, int rows, int B, int Hq, int Hkv, int D, int n_pages,
                  int64_t n_indices, int max_pages, int page_size, float scale, float softcap,
@@ -69,14 +74,14 @@ int check_attend(const void* q, int64_t q_stride, const void* k_cache, const voi
       return IDX_ERR_INVALID_ARG;
   }
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(kv_indptr, 4) ||
-      !aligned(kv_indices, 4) || !aligned(kv_len, 4) || !aligned(slopes, 4))
+      !aligned(k_scale, scale_align) || !aligned(v_scale, scale_align) ||
+      !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(kv_len, 4) || !aligned(slopes, 4))
     return IDX_ERR_INVALID_ARG;
   return IDX_OK;
 }
 
-idxk::AttnArgs attend_args(const void* q, int64_t q_stride, const uint8_t* k_cache,
-                           const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+idxk::AttnArgs attend_args(int bits, const void* q, int64_t q_stride, const uint8_t* k_cache,
+                           const uint8_t* v_cache, const void* k_scale, const void* v_scale,
                            const int32_t* kv_indptr, const int32_t* kv_indices,
                            const int32_t* kv_len, const float* slopes, void* out, int rows, int B,
                            int Hq, int Hkv, int n_pages, int64_t n_indices, int max_pages,
@@ -86,8 +91,13 @@ idxk::AttnArgs attend_args(const void* q, int64_t q_stride, const uint8_t* k_cac
   a.q_stride = q_stride;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
+  if (bits == 8) {
+    a.k_scale = static_cast<const float*>(k_scale);
+    a.v_scale = static_cast<const float*>(v_scale);
+  } else {
+    a.k_exp = static_cast<const uint8_t*>(k_scale);
+    a.v_exp = static_cast<const uint8_t*>(v_scale);
+  }
   a.kv_indptr = kv_indptr;
   a.kv_indices = kv_indices;
   a.kv_len = kv_len;
@@ -115,6 +125,118 @@ idxk::AttnArgs attend_args(const void* q, int64_t q_stride, const uint8_t* k_cac
 int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
     return IDX_ERR_WORKSPACE;
+  return IDX_OK;
+}
+
+// How the rows of a call are cut.
+idxk::AttnSplit single_split(int bits, int R, int Hkv, int64_t units) {
+  return bits == 8 ? idxk::attend_rows_split(R, Hkv, units)
+                   : idxk::attend4_rows_split(R, Hkv, units);
+}
+idxk::AttnSplit packed_split(int bits, int n_tok, int B, int Hq, int Hkv, int64_t units) {
+  return bits == 8 ? idxk::attend_prefill_split(n_tok, B, Hq, Hkv, units)
+                   : idxk::attend4_prefill_split(n_tok, B, Hq, Hkv, units);
+}
+
+size_t single_bytes(int bits, int R, int Hq, int Hkv, int max_pages, int K, int page_size) {
+  if (R < 1 || K < 0 || !shape_ok(R, 1, Hq, Hkv, max_pages, page_size)) return 0;
+  return partial_bytes(
+      R, Hq, single_split(bits, R, Hkv, row_units(max_pages, K, page_size)).splits);
+}
+
+// idx_attend over the cache of so many bits, and idx_attend_prefill
+int attend_single(int bits, const void* q, int64_t q_stride, const uint8_t* k_cache,
+                  const uint8_t* v_cache, const void* k_scale, const void* v_scale,
+                  const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* kv_len,
+                  const int32_t* row_req, const int32_t* ids, const float* slopes, void* out, int R,
+                  int B, int Hq, int Hkv, int D, int n_pages, int64_t n_indices, int max_pages,
+                  int page_size, int K, float scale, float softcap, idx_dtype dt, void* ws,
+                  size_t ws_bytes, void* stream) {
+  const int st = check_attend(q, q_stride, k_cache, v_cache, k_scale, v_scale, bits == 8 ? 4 : 16,
+                              kv_indptr, kv_indices, kv_len, slopes, out, R, B, Hq, Hkv, D,
+                              n_pages, n_indices, max_pages, page_size, scale, softcap, dt);
+  if (st != IDX_OK) return st;
+  if (!aligned(row_req, 4) || !aligned(ids, 4)) return IDX_ERR_INVALID_ARG;
+  if (K < 0 || (ids != nullptr) != (K > 0) || (row_req == nullptr && R > B))
+    return IDX_ERR_INVALID_ARG;
+  if ((int64_t)K * page_size > kMaxInt) return IDX_ERR_INVALID_ARG;
+  if (R == 0) return IDX_OK;
+  const idxk::AttnSplit sp = single_split(bits, R, Hkv, row_units(max_pages, K, page_size));
+  // 256 threads for each of at most two workgroups a row, KV head and split (rows are cut,
+  // and joined, only where rows times KV heads are a few hundred)
+  if ((int64_t)R * Hkv * sp.splits * (Hq / Hkv > 32 ? 2 : 1) * 256 > kMaxThreads)
+    return IDX_ERR_INVALID_ARG;
+  const int wst = check_workspace(ws, ws_bytes, partial_bytes(R, Hq, sp.splits));
+  if (wst != IDX_OK) return wst;
+  idxk::AttnArgs a = attend_args(bits, q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
+                                 kv_indices, kv_len, slopes, out, R, B, Hq, Hkv, n_pages,
+                                 n_indices, max_pages, page_size, scale, softcap, sp.splits, ws);
+  a.row_req = row_req;
+  a.ids = ids;
+  a.K = K;
+  return hip_status(bits == 8 ? idxk::launch_attend_rows(a, sp, stream)
+                              : idxk::launch_attend4_rows(a, sp, stream));
+}
+
+size_t packed_bytes(int bits, int n_tok, int B, int Hq, int Hkv, int max_pages, int page_size) {
+  if (n_tok < 1 || !shape_ok(n_tok, B, Hq, Hkv, max_pages, page_size)) return 0;
+  return partial_bytes(
+      n_tok, Hq, packed_split(bits, n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size)).splits);
+}
+
+int attend_packed(int bits, const void* q, int64_t q_stride, const uint8_t* k_cache,
+                  const uint8_t* v_cache, const void* k_scale, const void* v_scale,
+                  const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* tok_indptr,
+                  const int32_t* kv_len, const float* slopes, void* out, int n_tok, int B, int Hq,
+                  int Hkv, int D, int n_pages, int64_t n_indices, int max_pages, int page_size,
+                  float scale, float softcap, idx_dtype dt, void* ws, size_t ws_bytes,
+                  void* stream) {
+  const int st = check_attend(q, q_stride, k_cache, v_cache, k_scale, v_scale, bits == 8 ? 4 : 16,
+                              kv_indptr, kv_indices, kv_len, slopes, out, n_tok, B, Hq, Hkv, D,
+                              n_pages, n_indices, max_pages, page_size, scale, softcap, dt);
+  if (st != IDX_OK) return st;
+  if ((n_tok > 0 && tok_indptr == nullptr) || !aligned(tok_indptr, 4)) return IDX_ERR_INVALID_ARG;
+  if (B > IDX_MAX_REQUESTS) return IDX_ERR_UNSUPPORTED;
+  if (n_tok == 0) return IDX_OK;
+  const idxk::AttnSplit sp =
+      packed_split(bits, n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size));
+  // up to 512 threads for each row tile, KV head and split
+  if (idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits * 512 >
+      kMaxThreads)
+    return IDX_ERR_INVALID_ARG;
+  const int wst = check_workspace(ws, ws_bytes, partial_bytes(n_tok, Hq, sp.splits));
+  if (wst != IDX_OK) return wst;
+  idxk::AttnArgs a = attend_args(bits, q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
+                                 kv_indices, kv_len, slopes, out, n_tok, B, Hq, Hkv, n_pages,
+                                 n_indices, max_pages, page_size, scale, softcap, sp.splits, ws);
+  a.tok_indptr = tok_indptr;
+  return hip_status(bits == 8 ? idxk::launch_attend_prefill(a, sp, stream)
+                              : idxk::launch_attend4_prefill(a, sp, stream));
+}
+
+// What the write and the read of a cache check; the caller's own scales apart.
+int check_rows(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+               const int32_t* slots, const void* k_cache, const void* v_cache,
+               const void* k_scale, const void* v_scale, int scale_align, int n_tok, int Hkv,
+               int D, int n_pages, int page_size, idx_dtype dt, bool both) {
+  if (n_tok < 0 || Hkv < 1 || D < 1 || n_pages < 1 || page_size < 1) return IDX_ERR_INVALID_ARG;
+  if (dt != IDX_F32 && dt != IDX_BF16) return IDX_ERR_INVALID_ARG;
+  if (D != IDX_HEAD_DIM || !page_size_built(page_size)) return IDX_ERR_UNSUPPORTED;
+  if ((int64_t)n_pages * Hkv > kMaxInt || (int64_t)n_pages * page_size > kMaxInt ||
+      (int64_t)Hkv * D > kMaxInt ||
+      ((int64_t)n_tok / 16 + 1) * (((int64_t)Hkv + 1) / 2) * 256 > kMaxThreads)
+    return IDX_ERR_INVALID_ARG;
+  if (n_tok > 0) {
+    if (((k == nullptr || v == nullptr) && both) || slots == nullptr || k_cache == nullptr ||
+        v_cache == nullptr || k_scale == nullptr || v_scale == nullptr)
+      return IDX_ERR_INVALID_ARG;
+    for (int64_t stride : {k != nullptr ? k_stride : (int64_t)Hkv * D,
+                           v != nullptr ? v_stride : (int64_t)Hkv * D})
+      if (stride < (int64_t)Hkv * D || stride % 8 != 0) return IDX_ERR_INVALID_ARG;
+  }
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(k_scale, scale_align) || !aligned(v_scale, scale_align))
+    return IDX_ERR_INVALID_ARG;
   return IDX_OK;
 }
 
@@ -154,34 +276,43 @@ int idx_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_st
                     const int32_t* slots, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
                     float* v_scale, int n_tok, int Hkv, int D, int n_pages, int page_size,
                     idx_dtype dt, void* stream) {
-  if (n_tok < 0 || Hkv < 1 || D < 1 || n_pages < 1 || page_size < 1) return IDX_ERR_INVALID_ARG;
-  if (dt != IDX_F32 && dt != IDX_BF16) return IDX_ERR_INVALID_ARG;
-  if (D != IDX_HEAD_DIM || !page_size_built(page_size)) return IDX_ERR_UNSUPPORTED;
-  if ((int64_t)n_pages * Hkv > kMaxInt || (int64_t)n_pages * page_size > kMaxInt ||
-      (int64_t)Hkv * D > kMaxInt ||
-      ((int64_t)n_tok / 16 + 1) * (((int64_t)Hkv + 1) / 2) * 256 > kMaxThreads)
-    return IDX_ERR_INVALID_ARG;
-  if (n_tok > 0) {
-    if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr ||
-        v_cache == nullptr || k_scale == nullptr || v_scale == nullptr)
-      return IDX_ERR_INVALID_ARG;
-    if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 != 0 ||
-        v_stride % 8 != 0)
-      return IDX_ERR_INVALID_ARG;
-  }
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(k_cache, 16) ||
-      !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
-    return IDX_ERR_INVALID_ARG;
+  const int st = check_rows(k, v, k_stride, v_stride, slots, k_cache, v_cache, k_scale, v_scale, 4,
+                            n_tok, Hkv, D, n_pages, page_size, dt, true);
+  if (st != IDX_OK) return st;
   if (n_tok == 0) return IDX_OK;
   return hip_status(idxk::launch_cache_write(k, v, k_stride, v_stride, slots, k_cache, v_cache,
                                              k_scale, v_scale, n_tok, Hkv, n_pages, page_size,
                                              dt == IDX_BF16, stream));
 }
 
+int idx_cache4_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                     const int32_t* slots, uint8_t* k_cache, uint8_t* v_cache, uint8_t* k_scale,
+                     uint8_t* v_scale, int n_tok, int Hkv, int D, int n_pages, int page_size,
+                     idx_dtype dt, void* stream) {
+  const int st = check_rows(k, v, k_stride, v_stride, slots, k_cache, v_cache, k_scale, v_scale,
+                            16, n_tok, Hkv, D, n_pages, page_size, dt, true);
+  if (st != IDX_OK) return st;
+  if (n_tok == 0) return IDX_OK;
+  return hip_status(idxk::launch_cache4_write(k, v, k_stride, v_stride, slots, k_cache, v_cache,
+                                              k_scale, v_scale, n_tok, Hkv, n_pages, page_size,
+                                              dt == IDX_BF16, stream));
+}
+
+int idx_cache4_read(const int32_t* slots, const uint8_t* k_cache, const uint8_t* v_cache,
+                    const uint8_t* k_scale, const uint8_t* v_scale, void* k, void* v,
+                    int64_t k_stride, int64_t v_stride, int n_tok, int Hkv, int D, int n_pages,
+                    int page_size, idx_dtype dt, void* stream) {
+  const int st = check_rows(k, v, k_stride, v_stride, slots, k_cache, v_cache, k_scale, v_scale,
+                            16, n_tok, Hkv, D, n_pages, page_size, dt, false);
+  if (st != IDX_OK) return st;
+  if (n_tok == 0 || (k == nullptr && v == nullptr)) return IDX_OK;
+  return hip_status(idxk::launch_cache4_read(slots, k_cache, v_cache, k_scale, v_scale, k, v,
+                                             k_stride, v_stride, n_tok, Hkv, n_pages, page_size,
+                                             dt == IDX_BF16, stream));
+}
+
 size_t idx_attend_workspace_bytes(int R, int Hq, int Hkv, int max_pages, int K, int page_size) {
-  if (R < 1 || K < 0 || !shape_ok(R, 1, Hq, Hkv, max_pages, page_size)) return 0;
-  return partial_bytes(
-      R, Hq, idxk::attend_rows_split(R, Hkv, row_units(max_pages, K, page_size)).splits);
+  return single_bytes(8, R, Hq, Hkv, max_pages, K, page_size);
 }
 
 int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -190,38 +321,30 @@ int idx_attend(const void* q, int64_t q_stride, const uint8_t* k_cache, const ui
                const int32_t* ids, const float* slopes, void* out, int R, int B, int Hq, int Hkv,
                int D, int n_pages, int64_t n_indices, int max_pages, int page_size, int K,
                float scale, float softcap, idx_dtype dt, void* ws, size_t ws_bytes, void* stream) {
-  const int st = check_attend(q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
-                              kv_indices, kv_len, slopes, out, R, B, Hq, Hkv, D, n_pages,
-                              n_indices, max_pages, page_size, scale, softcap, dt);
-  if (st != IDX_OK) return st;
-  if (!aligned(row_req, 4) || !aligned(ids, 4)) return IDX_ERR_INVALID_ARG;
-  if (K < 0 || (ids != nullptr) != (K > 0) || (row_req == nullptr && R > B))
-    return IDX_ERR_INVALID_ARG;
-  if ((int64_t)K * page_size > kMaxInt) return IDX_ERR_INVALID_ARG;
-  if (R == 0) return IDX_OK;
-  const idxk::AttnSplit sp =
-      idxk::attend_rows_split(R, Hkv, row_units(max_pages, K, page_size));
-  // 256 threads for each of at most two workgroups a row, KV head and split (rows are cut,
-  // and joined, only where rows times KV heads are a few hundred)
-  if ((int64_t)R * Hkv * sp.splits * (Hq / Hkv > 32 ? 2 : 1) * 256 > kMaxThreads)
-    return IDX_ERR_INVALID_ARG;
-  const int wst = check_workspace(ws, ws_bytes, partial_bytes(R, Hq, sp.splits));
-  if (wst != IDX_OK) return wst;
-  idxk::AttnArgs a = attend_args(q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
-                                 kv_indices, kv_len, slopes, out, R, B, Hq, Hkv, n_pages,
-                                 n_indices, max_pages, page_size, scale, softcap, sp.splits, ws);
-  a.row_req = row_req;
-  a.ids = ids;
-  a.K = K;
-  return hip_status(idxk::launch_attend_rows(a, sp, stream));
+  return attend_single(8, q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                       kv_len, row_req, ids, slopes, out, R, B, Hq, Hkv, D, n_pages, n_indices,
+                       max_pages, page_size, K, scale, softcap, dt, ws, ws_bytes, stream);
+}
+
+size_t idx_attend4_workspace_bytes(int R, int Hq, int Hkv, int max_pages, int K, int page_size) {
+  return single_bytes(4, R, Hq, Hkv, max_pages, K, page_size);
+}
+
+int idx_attend4(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* kv_indptr,
+                const int32_t* kv_indices, const int32_t* kv_len, const int32_t* row_req,
+                const int32_t* ids, const float* slopes, void* out, int R, int B, int Hq, int Hkv,
+                int D, int n_pages, int64_t n_indices, int max_pages, int page_size, int K,
+                float scale, float softcap, idx_dtype dt, void* ws, size_t ws_bytes,
+                void* stream) {
+  return attend_single(4, q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                       kv_len, row_req, ids, slopes, out, R, B, Hq, Hkv, D, n_pages, n_indices,
+                       max_pages, page_size, K, scale, softcap, dt, ws, ws_bytes, stream);
 }
 
 size_t idx_attend_prefill_workspace_bytes(int n_tok, int B, int Hq, int Hkv, int max_pages,
                                           int page_size) {
-  if (n_tok < 1 || !shape_ok(n_tok, B, Hq, Hkv, max_pages, page_size)) return 0;
-  return partial_bytes(
-      n_tok, Hq,
-      idxk::attend_prefill_split(n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size)).splits);
+  return packed_bytes(8, n_tok, B, Hq, Hkv, max_pages, page_size);
 }
 
 int idx_attend_prefill(const void* q, int64_t q_stride, const uint8_t* k_cache,
@@ -231,26 +354,26 @@ int idx_attend_prefill(const void* q, int64_t q_stride, const uint8_t* k_cache,
                        void* out, int n_tok, int B, int Hq, int Hkv, int D, int n_pages,
                        int64_t n_indices, int max_pages, int page_size, float scale,
                        float softcap, idx_dtype dt, void* ws, size_t ws_bytes, void* stream) {
-  const int st = check_attend(q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
-                              kv_indices, kv_len, slopes, out, n_tok, B, Hq, Hkv, D, n_pages,
-                              n_indices, max_pages, page_size, scale, softcap, dt);
-  if (st != IDX_OK) return st;
-  if ((n_tok > 0 && tok_indptr == nullptr) || !aligned(tok_indptr, 4)) return IDX_ERR_INVALID_ARG;
-  if (B > IDX_MAX_REQUESTS) return IDX_ERR_UNSUPPORTED;
-  if (n_tok == 0) return IDX_OK;
-  const idxk::AttnSplit sp =
-      idxk::attend_prefill_split(n_tok, B, Hq, Hkv, row_units(max_pages, 0, page_size));
-  // up to 512 threads for each row tile, KV head and split
-  if (idxk::attend_prefill_tiles(n_tok, B, Hq / Hkv, sp.rows) * Hkv * sp.splits * 512 >
-      kMaxThreads)
-    return IDX_ERR_INVALID_ARG;
-  const int wst = check_workspace(ws, ws_bytes, partial_bytes(n_tok, Hq, sp.splits));
-  if (wst != IDX_OK) return wst;
-  idxk::AttnArgs a = attend_args(q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr,
-                                 kv_indices, kv_len, slopes, out, n_tok, B, Hq, Hkv, n_pages,
-                                 n_indices, max_pages, page_size, scale, softcap, sp.splits, ws);
-  a.tok_indptr = tok_indptr;
-  return hip_status(idxk::launch_attend_prefill(a, sp, stream));
+  return attend_packed(8, q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                       tok_indptr, kv_len, slopes, out, n_tok, B, Hq, Hkv, D, n_pages, n_indices,
+                       max_pages, page_size, scale, softcap, dt, ws, ws_bytes, stream);
+}
+
+size_t idx_attend4_prefill_workspace_bytes(int n_tok, int B, int Hq, int Hkv, int max_pages,
+                                           int page_size) {
+  return packed_bytes(4, n_tok, B, Hq, Hkv, max_pages, page_size);
+}
+
+int idx_attend4_prefill(const void* q, int64_t q_stride, const uint8_t* k_cache,
+                        const uint8_t* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                        const int32_t* kv_indptr, const int32_t* kv_indices,
+                        const int32_t* tok_indptr, const int32_t* kv_len, const float* slopes,
+                        void* out, int n_tok, int B, int Hq, int Hkv, int D, int n_pages,
+                        int64_t n_indices, int max_pages, int page_size, float scale,
+                        float softcap, idx_dtype dt, void* ws, size_t ws_bytes, void* stream) {
+  return attend_packed(4, q, q_stride, k_cache, v_cache, k_scale, v_scale, kv_indptr, kv_indices,
+                       tok_indptr, kv_len, slopes, out, n_tok, B, Hq, Hkv, D, n_pages, n_indices,
+                       max_pages, page_size, scale, softcap, dt, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -93,6 +93,34 @@ AttnSplit attend_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t un
 int64_t attend_prefill_tiles(int64_t n_tok, int B, int G, int per);  // of `per` rows
 int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
+// the 4-bit cache (idx_attend4, idx_attend4_prefill)
+AttnSplit attend4_rows_split(int64_t R, int Hkv, int64_t units);
+AttnSplit attend4_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units);
+int launch_attend4_rows(const AttnArgs& a, AttnSplit sp, void* stream);
+int launch_attend4_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend_merge(const AttnArgs& a, int splits, void* stream);
+
+// The 4-bit cache's write and its reading back (idx_cache4_write, idx_cache4_read).
+int launch_cache4_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                        const int32_t* slots, uint8_t* k_cache, uint8_t* v_cache,
+                        uint8_t* k_scale, uint8_t* v_scale, int n_tok, int Hkv, int n_pages,
+                        int page_size, bool bf16, void* stream);
+int launch_cache4_read(const int32_t* slots, const uint8_t* k_cache, const uint8_t* v_cache,
+                       const uint8_t* k_scale, const uint8_t* v_scale, void* k, void* v,
+                       int64_t k_stride, int64_t v_stride, int n_tok, int Hkv, int n_pages,
+                       int page_size, bool bf16, void* stream);
+
+// Rotary positions (idx_rope).
+struct RopeArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t* tok_len;
+  const uint64_t* turns;
+  int n_tok, Hq, Hkv, first, rot;
+  float factor;
+  bool adjacent, inverse;
+};
+int launch_rope(const RopeArgs& a, bool bf16, void* stream);
 
 }  // namespace idxk
