@@ -24,7 +24,7 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", os.path.joi
 
 HIP_SOURCES = ["indexer.hip", "indexer_radix8.hip", "assign.hip", "prefill.hip", "pool.hip",
                "floor.hip", "tables.hip", "cache_write.hip", "attend.hip", "attend_prefill.hip",
-               "cache4.hip", "attend4.hip", "rope.hip"]
+               "cache4.hip", "attend4.hip", "attend4_prefill.hip", "rope.hip"]
 # assign.hip's inputs are finite by contract; without NaN semantics its running
 # max compiles to plain 3-input maxes (no per-operand canonicalisation)
 EXTRA_FLAGS = {"assign.hip": ["-fno-honor-nans"]}

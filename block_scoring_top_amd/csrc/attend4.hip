@@ -13,16 +13,6 @@ AttnSplit attend4_rows_split(int64_t R, int Hkv, int64_t units) {
   return attend_rows_split(R, Hkv, units);
 }
 
-AttnSplit attend4_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
-  AttnSplit sp = attend4_rows_split(attend_prefill_tiles(n_tok, B, Hq / Hkv, 16), Hkv, units);
-  sp.rows = 16;
-  return sp;
-}
-
-int launch_attend4_prefill(const AttnArgs& a, AttnSplit sp, void* stream) {
-  return launch_attend4_rows(a, sp, stream);
-}
-
 int launch_attend4_rows(const AttnArgs& a, AttnSplit sp, void* stream) {
   return launch_rows_of<Cache4>(a, sp, stream);
 }

@@ -1,0 +1,473 @@
+// Attention of packed prompt tokens over the paged 4-bit cache (include/idx_cache4.h,
+// idx_attend4_prefill). The split of the work, the products and the layout of their operands
+// in LDS are those of attend_prefill.hip: a workgroup owns kP4Rows rows (token, head of the
+// KV head's group) of one request, 32 to a wave, and walks its tokens in tiles of 64, whose
+// codes are converted once, on their way into LDS.
+//   - Keys become bf16 with their scales, exact.
+//   - Values become fp16. In a tile that all rows see whole, a value takes its scale along,
+//     relative to the largest of the 16 tokens' (of its unit, 2^lv), and 2^lv enters with the
+//     exponential's argument and leaves the sum of weights once a unit. In one that some
+//     rows see in part (the end of each row), values stay plain codes, and the scales of the
+//     tokens that a row sees go to its probabilities, a group of 32 dims at a time, as in
+//     attend4.hpp: nothing of a row comes from tokens that it does not see, and a NaN scale
+//     reaches just the rows that see it.
+//   - The reference of a row's sums is the running maximum of score + lv, moved when it has
+//     grown by 2^kLazy or more.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "attend4.hpp"
+#include "launch.h"
+
+namespace idxk {
+
+typedef float at_f32x16 __attribute__((ext_vector_type(16)));
+
+namespace {
+
+constexpr int kP4Waves = 8;
+constexpr int kP4NT = kP4Waves * kWave;
+constexpr int kP4Rows = 32 * kP4Waves;
+constexpr int kP4PackedMean = 64;              // rows a request, up to which they are few
+constexpr int kP4CUs = 256;
+constexpr int kP4Phase = 512;                  // tiles whose pages wait in LDS
+constexpr int kP4Units = 4 * (kP4Phase + 4);   // and of the tiles loaded ahead
+constexpr int kP4Ahead = 4;                    // operands read from LDS before their use
+constexpr int kP4Frag = kWave;                 // uint4s of one operand in LDS
+
+struct Pre4Lds {
+  uint4 k[2][16][kP4Frag];  // [buffer][32-token half, 16-dim step]
+  uint4 v[2][16][kP4Frag];  // [buffer][32-dim tile, 32-token half, 8 tokens of the units]
+  uint4 scales[2][4][4];    // of the values: [buffer][unit][32 dims], a byte a token
+  uint32_t top[2][4];       // the units' largest
+  int u_blk[kP4Units];
+  int longest[kP4Waves], shortest[kP4Waves];
+  unsigned long long work[kP4Waves];
+  int found;
+};
+
+__device__ __forceinline__ float p4_halves_max(float v) {
+  return fmaxf(v, __uint_as_float(lane_xor<32>(__float_as_uint(v))));
+}
+
+// eight words of fp16 scales (token pairs of a unit) from its bytes of a group of dims
+__device__ __forceinline__ void unit_scales(uint4 bytes, uint32_t floor2, bool nan,
+                                            uint32_t (&s)[8]) {
+  const uint32_t w[4] = {bytes.x, bytes.y, bytes.z, bytes.w};
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    s[2 * t] = two_scales<0>(w[t], floor2);
+    s[2 * t + 1] = two_scales<1>(w[t], floor2);
+  }
+  if (nan) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t pair = w[t >> 1] >> (16 * (t & 1));
+      if ((pair & 255u) == kNanScale) s[t] = (s[t] & 0xFFFF0000u) | 0x7E00u;
+      if (((pair >> 8) & 255u) == kNanScale) s[t] = (s[t] & 0xFFFFu) | 0x7E000000u;
+    }
+  }
+}
+
+// the bytes of the tokens that a row sees of 16
+__device__ __forceinline__ uint4 seen_bytes(uint4 w, int have) {
+  return make_uint4(keep_bytes(w.x, have), keep_bytes(w.y, have - 4), keep_bytes(w.z, have - 8),
+                    keep_bytes(w.w, have - 12));
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int chunk, int splits,
+                                                                int64_t n_tiles) {
+  __shared__ Pre4Lds lds;
+  const int h = blockIdx.x % a.Hkv;
+  const int rest = blockIdx.x / a.Hkv;
+  // the row tiles of one stretch of keys side by side: they share it in L2, one KV head to
+  // an XCD where there are eight (or the heads divide them); a prompt's last tokens, which
+  // see most, first
+  const int split = (int)(rest / n_tiles);
+  const int64_t tile = n_tiles - 1 - rest % n_tiles;
+  const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
+  const int n = lane & 31, half = lane >> 5;
+  const int G = a.Hq / a.Hkv;
+  const int ush = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(units a page)
+
+  const RowTile rt = row_tile<kP4NT>(a, tile, G, kP4Rows, &lds.found);
+  const int t0 = rt.t0;
+  const int64_t row0 = rt.row0, rows = rt.rows;
+  if (row0 < 0 || row0 >= rows) return;
+
+  const PageList pages = page_list(a, rt.b);
+  const int64_t row = row0 + 32 * w + n;
+  const int64_t rat = min(row, rows - 1);
+  const int64_t tok = t0 + rat / G;
+  const int hq = h * G + (int)(rat % G);
+  const int len = row < rows ? max(a.kv_len[tok], 0) : 0;
+  const float slope2 = KIND != kPlain ? slope_of(a, hq) : 0.f;
+  // dims 16 s + 8 half .. + 7 of the row; a negative call scale turns the queries' signs
+  at_bf16x8 q[8];
+  {
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + hq * kHeadDim);
+    const uint32_t sign = a.score_scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint4 x = p[2 * s + half];
+      q[s] = __builtin_bit_cast(at_bf16x8,
+                                make_uint4(x.x ^ sign, x.y ^ sign, x.z ^ sign, x.w ^ sign));
+    }
+  }
+  const float call_scale = fabsf(a.score_scale);
+  const Cap cap(a.softcap);
+
+  int longest = len, shortest = row < rows ? len : 0x7FFFFFFF;  // of the wave's rows
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    longest = max(longest, __shfl_xor(longest, d));
+    shortest = min(shortest, __shfl_xor(shortest, d));
+  }
+  // A cut call's stretches (attend_prefill.hip): lengthened to a CU's share of the call
+  unsigned long long work = 0;
+  if (splits > 1) {
+    for (int i = tid; i < a.B; i += kP4NT) {
+      const int x0 = min(max(a.tok_indptr[i], 0), a.R);
+      const int x1 = min(max(a.tok_indptr[i + 1], 0), a.R);
+      if (x1 <= x0) continue;
+      const int64_t held = (int64_t)page_list(a, i).n * a.page_size;
+      const int64_t seen = min(held, (int64_t)max(a.kv_len[x0], 0)) +
+                           min(held, (int64_t)max(a.kv_len[x1 - 1], 0));
+      work += (((int64_t)(x1 - x0) * G + kP4Rows - 1) / kP4Rows) *
+              ((seen / 2 + kTileTok - 1) / kTileTok);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) work += __shfl_xor(work, d);
+  }
+  if (lane == 0) {
+    lds.longest[w] = longest;
+    lds.shortest[w] = shortest;
+    lds.work[w] = work;
+  }
+  __syncthreads();
+  int most = 0, least = 0x7FFFFFFF;  // of the workgroup's rows
+  work = 0;
+#pragma unroll
+  for (int i = 0; i < kP4Waves; ++i) {
+    most = max(most, lds.longest[i]);
+    least = min(least, lds.shortest[i]);
+    work += lds.work[i];
+  }
+  if (splits > 1)
+    chunk = (int)min((unsigned long long)0x7FFFFFFF,
+                     max((unsigned long long)chunk, (work * a.Hkv + kP4CUs - 1) / kP4CUs));
+
+  const int units = min(pages.n << ush, (int)(((int64_t)most + kUnit - 1) / kUnit));
+  const int64_t end = min(((int64_t)units + 3) / 4, ((int64_t)split + 1) * chunk);
+  int begin = 0, count = 0;  // the phase's tiles
+  // whether some rows see tile c of the phase in part
+  auto in_part = [&](int c) { return (int64_t)(begin + c + 1) * kTileTok > least; };
+
+  // staging: thread -> (token, 16 dims) of the keys and (unit, dim) of the values
+  const int sub = (1 << ush) - 1;
+  const int hp = a.page_size / 2;
+  const int ktok = (tid & 7) | ((tid >> 6) << 3), kc = (tid >> 3) & 7;  // 8 tokens a wave
+  const int ku = ktok >> 4;
+  const int vd = tid & 127, vu = tid >> 7;
+  const int su = lane >> 4;  // this lane's unit, and word, of the values' scales
+  uint2 kreg, vreg;
+  uint4 vscale;
+  uint32_t kscale, word;
+  auto load_k = [&](int c) {  // c: tile of the phase
+    const int kb = lds.u_blk[4 * c + ku];
+    const int64_t at = (int64_t)max(kb, 0) * a.page_size +
+                       (((4 * (begin + c) + ku) & sub) * kUnit + (ktok & 15));
+    kreg = *reinterpret_cast<const uint2*>(a.k_cache + at * (kHeadDim / 2) + 8 * kc);
+    kscale = a.k_exp[at * 4 + (kc >> 1)];
+    if (kb < 0) kreg = make_uint2(0, 0), kscale = 127;
+  };
+  auto load_v = [&](int c) {
+    const int vb = lds.u_blk[4 * c + vu], u = 4 * (begin + c) + vu;
+    vreg = *reinterpret_cast<const uint2*>(a.v_cache + (int64_t)max(vb, 0) * (kHeadDim * hp) +
+                                           (vd * hp + (u & sub) * (kUnit / 2)));
+    vscale = *reinterpret_cast<const uint4*>(
+        a.v_exp + ((int64_t)max(vb, 0) * 4 + (vd >> 5)) * a.page_size + (u & sub) * kUnit);
+    const int sb = lds.u_blk[4 * c + su], s = 4 * (begin + c) + su;
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(
+        a.v_exp + ((int64_t)max(sb, 0) * 4 + ((lane >> 2) & 3)) * a.page_size +
+        (s & sub) * kUnit + 4 * (lane & 3));
+    if (vb < 0) vscale = make_uint4(0, 0, 0, 0);
+    word = sb < 0 ? 0u : x;
+  };
+  auto store_k = [&](int c) {
+    // row 8 q + 4 (unit of the 32) + e holds token 4 q + e; every other step swaps rows 4
+    // apart, so that 16 lanes' stores meet 16 different banks of 16 bytes
+    const int i = ktok & 15, m32 = 8 * (i >> 2) + 4 * (ku & 1) + (i & 3);
+    const float s = __uint_as_float(kscale << 23);
+    uint4* p = &lds.k[c & 1][(ku >> 1) * 8 + kc][m32 ^ ((kc & 1) << 2)];
+    p[0] = __builtin_bit_cast(uint4, codes4_bf16(kreg.x, s));
+    p[32] = __builtin_bit_cast(uint4, codes4_bf16(kreg.y, s));
+  };
+  auto store_v = [&](int c) {
+    uint4 x[2] = {__builtin_bit_cast(uint4, codes4_f16(vreg.x)),
+                  __builtin_bit_cast(uint4, codes4_f16(vreg.y))};
+    if (in_part(c)) {
+      if (w == 0)
+        reinterpret_cast<uint32_t*>(&lds.scales[c & 1][su][(lane >> 2) & 3])[lane & 3] = word;
+    } else {
+      const uint32_t top = max(group_max(top_byte(word)), 15u);
+      const uint32_t mine = (uint32_t)__builtin_amdgcn_readlane((int)top, 16 * (w >> 1));
+      uint32_t s[8];
+      unit_scales(vscale, (mine - 15u) * 0x00010001u, __any(nan_scales(word) != 0), s);
+      uint32_t* y = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = mul_f16(y[i], s[i]);
+      if (w == 0 && (lane & 15) == 0) lds.top[c & 1][su] = top;
+    }
+    uint4* p = &lds.v[c & 1][((vd >> 5) * 2 + (vu >> 1)) * 2][(vu & 1) * 32 + (vd & 31)];
+    p[0] = x[0];
+    p[kP4Frag] = x[1];
+  };
+
+  // the wave's state: sums in units of 2^m
+  at_f32x16 o[4];
+#pragma unroll
+  for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+  float m = -__builtin_inff(), l = 0.f;
+
+  // operands are read from LDS kP4Ahead products before their use
+  auto products = [&](at_f32x16 (&x)[2], int c) {
+    auto read = [&](int i) {
+      return __builtin_bit_cast(at_bf16x8, lds.k[c & 1][i][lane ^ ((i & 1) << 2)]);
+    };
+    at_bf16x8 f[16];
+#pragma unroll
+    for (int i = 0; i < kP4Ahead; ++i) f[i] = read(i);
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[ts][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + kP4Ahead < 16) f[i + kP4Ahead] = read(i + kP4Ahead);
+      x[i >> 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i], q[i & 7], x[i >> 3], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, kP4Ahead, 0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + kP4Ahead < 16) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+  };
+  auto step = [&](int c, auto part_of) {
+    constexpr bool part = decltype(part_of)::value;
+    at_f32x16 x[2];
+    products(x, c);
+    __builtin_amdgcn_sched_barrier(0);
+    // maxima, masks and the reference
+    int have[2];
+    uint32_t top[2];
+    float lv[2];
+    bool nan = false;
+    float best = -__builtin_inff();
+    const float sc = KIND != kPlain ? 1.f : fmaxf(call_scale, 0x1p-126f);
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      const int i = 4 * c + 2 * ts + half, pos = (4 * begin + i) * kUnit;
+      have[ts] = lds.u_blk[i] < 0 ? 0 : min(kUnit, len - pos);
+      if constexpr (!part) {
+        top[ts] = lds.top[c & 1][2 * ts + half];
+      } else {
+        uint32_t bad = 0;
+        top[ts] = 15u;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint4 s = seen_bytes(lds.scales[c & 1][2 * ts + half][d], have[ts]);
+          top[ts] = max(max(max(top[ts], top_byte(s.x)), max(top_byte(s.y), top_byte(s.z))),
+                        top_byte(s.w));
+          bad |= nan_scales(s.x) | nan_scales(s.y) | nan_scales(s.z) | nan_scales(s.w);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        nan |= __any(bad != 0);
+      }
+      lv[ts] = (float)((int)top[ts] - 127);
+      if constexpr (KIND != kPlain) {
+        const float bias = -slope2 * (float)(len - 1 - pos);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float c0 = __builtin_fmaf((float)j, slope2, bias);
+          x[ts][j] = score2<KIND>(x[ts][j], call_scale, cap, c0);
+        }
+      }
+    }
+    if (__any(have[0] < kUnit || have[1] < kUnit)) {
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[ts][j] = j < have[ts] ? x[ts][j] : -__builtin_inff();
+    }
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      float mx = x[ts][0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) mx = fmaxf(mx, x[ts][j]);
+      best = fmaxf(best, __builtin_fmaf(mx, sc, lv[ts]));
+    }
+    best = p4_halves_max(best);
+    if (__any(best > m + kLazy)) {
+      const float mn = best > m + kLazy ? best : m;
+      const float f = exp2_fast(m - (mn == -__builtin_inff() ? 0.f : mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < 4; ++dt) o[dt] *= f;
+    }
+    auto read = [&](int i) {  // 8 tokens a quarter, dims 32 (i % 4) ..
+      return __builtin_bit_cast(at_f16x8, lds.v[c & 1][(i & 3) * 4 + (i >> 2)][lane]);
+    };
+    at_f16x8 f[16];
+    if constexpr (!part) {
+#pragma unroll
+      for (int i = 0; i < kP4Ahead; ++i) f[i] = read(i);
+    }
+    const float base = m == -__builtin_inff() ? 0.f : m;
+    uint4 p[4];
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      const float off = base - kPBias - lv[ts];
+      float sum = 0.f;
+      uint32_t wd[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e0 = exp2_fast(__builtin_fmaf(x[ts][2 * i], sc, -off));
+        const float e1 = exp2_fast(__builtin_fmaf(x[ts][2 * i + 1], sc, -off));
+        sum += e0 + e1;
+        wd[i] = pack_f16(e0, e1);
+      }
+      l = __builtin_fmaf(sum, __uint_as_float((254u - top[ts]) << 23), l);
+      p[2 * ts] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+      p[2 * ts + 1] = make_uint4(wd[4], wd[5], wd[6], wd[7]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!part) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i + kP4Ahead < 16) f[i + kP4Ahead] = read(i + kP4Ahead);
+        o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            f[i], __builtin_bit_cast(at_f16x8, p[i >> 2]), o[i & 3], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i + kP4Ahead < 16) __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+      }
+    } else {
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          uint32_t s[8];
+          unit_scales(seen_bytes(lds.scales[c & 1][2 * ts + half][d], have[ts]),
+                      (top[ts] - 15u) * 0x00010001u, nan, s);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 y = p[2 * ts + e];
+            const uint4 z = make_uint4(mul_f16(y.x, s[4 * e]), mul_f16(y.y, s[4 * e + 1]),
+                                       mul_f16(y.z, s[4 * e + 2]), mul_f16(y.w, s[4 * e + 3]));
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                read(4 * (2 * ts + e) + d), __builtin_bit_cast(at_f16x8, z), o[d], 0, 0, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);  // few tiles: no registers for it
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  for (int64_t at = (int64_t)split * chunk; at < end; at += kP4Phase) {
+    begin = (int)at;
+    count = (int)min(end - at, (int64_t)kP4Phase);
+    // the tiles any row of the wave sees
+    const int mine =
+        (int)min((int64_t)count, ((int64_t)longest + kTileTok - 1) / kTileTok - begin);
+    __syncthreads();  // the phase before has been read
+    for (int i = tid; i < 4 * (count + 4); i += kP4NT) {
+      const int u = 4 * begin + i;
+      lds.u_blk[i] = i < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
+    }
+    __syncthreads();
+    load_k(0);
+    load_v(0);
+    store_k(0);
+    store_v(0);
+    load_k(1);
+    load_v(1);
+    auto tiles = [&](int from, int to, auto part_of) {
+      for (int c = from; c < to; ++c) {
+        __syncthreads();  // tile c is written, tile c - 1 read
+        if (c < mine) step(c, part_of);
+        store_k(c + 1);
+        store_v(c + 1);
+        load_k(c + 2);
+        load_v(c + 2);
+      }
+    };
+    const int whole = (int)min((int64_t)count, max((int64_t)least / kTileTok - begin, (int64_t)0));
+    tiles(0, whole, std::false_type{});
+    tiles(whole, count, std::true_type{});
+  }
+
+  l += __uint_as_float(lane_xor<32>(__float_as_uint(l)));
+  if (row >= rows) return;
+  // lane: dims 32 dt + 8 q + 4 half + e of its row
+  if (splits == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* out = a.out + (tok * a.Hq + hq) * kHeadDim;
+#pragma unroll
+    for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<uint2*>(out + 32 * dt + 8 * g + 4 * half) =
+            make_uint2(pack_bf16(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv),
+                       pack_bf16(o[dt][4 * g + 2] * inv, o[dt][4 * g + 3] * inv));
+  } else {
+    const int64_t part = (((tok * a.Hkv + h) * splits) + split) * G + hq % G;
+    float* out = a.part_o + part * kHeadDim;
+#pragma unroll
+    for (int dt = 0; dt < 4; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<at_f32x4*>(out + 32 * dt + 8 * g + 4 * half) =
+            at_f32x4{o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]};
+    if (half == 0) {
+      a.part_ml[2 * part] = m;
+      a.part_ml[2 * part + 1] = l;
+    }
+  }
+}
+
+}  // namespace
+
+// How packed calls are cut: as the 8-bit cache's.
+AttnSplit attend4_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
+  return attend_prefill_split(n_tok, B, Hq, Hkv, units);
+}
+
+int launch_attend4_prefill(const AttnArgs& a, AttnSplit sp, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (sp.rows != kP4Rows) return launch_attend4_rows(a, sp, stream);
+  const int64_t tiles = attend_prefill_tiles(a.R, a.B, a.Hq / a.Hkv, kP4Rows);
+  const dim3 grid((unsigned)(tiles * a.Hkv * sp.splits)), blk(kP4NT);
+#define IDX_PRE4(KIND)                                                                         \
+  hipLaunchKernelGGL((attend4_prefill_kernel<KIND>), grid, blk, 0, s, a, sp.chunk, sp.splits, \
+                     tiles)
+  if (a.softcap > kNearCap) IDX_PRE4(kCappedFar);
+  else if (a.softcap > 0.f) IDX_PRE4(kCapped);
+  else if (a.slopes != nullptr) IDX_PRE4(kBiased);
+  else IDX_PRE4(kPlain);
+#undef IDX_PRE4
+  int e = (int)hipGetLastError();
+  if (e == 0 && sp.splits > 1) e = launch_attend_merge(a, sp.splits, stream);
+  return e;
+}
+
+}  // namespace idxk
