@@ -15,6 +15,7 @@ namespace {
 // A lane's part of a tile: its key bytes (unit n / 4), value bytes (unit g) and that unit's
 // scales.
 struct Cache8 {
+  struct Scratch {};
   struct Tile {
     uint4 k[4][2], v[8];
     float ks, vs;
@@ -41,7 +42,8 @@ struct Cache8 {
     template <int NT, int KIND, bool MIXED>
     __device__ __forceinline__ void add(AttnState<NT>& st, const at_bf16x8 (&q)[NT][4], int vblk,
                                         float call_scale, int pos, int have, const int (&len)[NT],
-                                        const float (&slope2)[NT], const Cap& cap, bool any) {
+                                        const float (&slope2)[NT], const Cap& cap, bool any,
+                                        Scratch&) {
       attn_tile<NT, KIND, MIXED>(st, q, k, v, vblk < 0 ? 0.f : ks * call_scale,
                                  vblk < 0 ? 0.f : vs, pos, have, len, slope2, cap, any);
     }
@@ -52,6 +54,11 @@ struct Cache8 {
   }
   template <int NT>
   static __device__ __forceinline__ void init(AttnState<NT>&) {}
+  static __device__ __forceinline__ int dim_of(int dt, int g) { return 16 * dt + 4 * g; }
+  template <int NT>
+  static __device__ __forceinline__ at_f32x4 sums(const AttnState<NT>& st, int j, int dt) {
+    return st.o[j][dt];
+  }
 };
 
 // The splits' sums of one (row, query head), each in units of its own maximum: TEAMS

@@ -11,7 +11,8 @@
 //     Their scales, a byte for each token and 32 dims, go to the probabilities: once for
 //     each of the four groups of 32 dims, as packed fp16 products with
 //     S = 2^(scale - the unit's largest scale), exact, and the unit's largest enters with
-//     the exponential's argument.
+//     the exponential's argument. The 16 lanes of a group make the factors of four tokens and
+//     32 dims each, and hand them to each other in LDS.
 // The reference of a row's sums is the running maximum of score + log2(the unit's largest
 // value scale): what it bounds is the products of weight and value, not the weights, so
 // that one token with large values and no weight costs the others no bits. Both the sums
@@ -85,13 +86,30 @@ __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
                                           __builtin_bit_cast(at_f16x2, b));
 }
 
+// the four bytes' largest, and over the 16 lanes of a group
+__device__ __forceinline__ uint32_t group_top(uint32_t w) {
+  return group_max(max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)));
+}
+
+// Between one lane's store to LDS and another's load, in one wave: LDS takes a wave's
+// accesses in order, the compiler has to as well.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 struct Cache4 {
+  // A unit's value scales, and those as fp16 factors: written by the 16 lanes of its group, a
+  // word of four tokens each, read by all of them.
+  struct Scratch {
+    uint4 bytes[4][4];    // [unit][32 dims], a byte a token
+    uint2 factor[4][16];  // [unit][32 dims, four tokens]
+  };
   struct Tile {
     uint4 k[4];       // token 4 s + n % 4 of unit n / 4, dims 32 g ..
     uint32_t ks[4];   // their scales
-    uint2 v[8];       // the 16 tokens of unit g at dim 16 dt + n
-    uint4 vs[4];      // the 16 tokens' scales of dims 32 i ..
-    uint32_t top;     // a word of vs: together the group's lanes hold each of them once
+    uint2 v[8];       // the 16 tokens of unit g at dim 32 (i / 2) + 2 n + i % 2
+    uint32_t vs;      // four tokens' value scales: dims 32 (n / 4) .., tokens 4 (n % 4) ..
 
     __device__ __forceinline__ void load(const AttnArgs& a, int kblk, int ksub, int vblk, int vsub,
                                          int n, int g) {
@@ -99,6 +117,9 @@ struct Cache4 {
       const int64_t row = kb * a.page_size + ksub * kUnit + (n & 3);
       const uint8_t* kp = a.k_cache + row * (kHeadDim / 2) + 16 * g;
       const uint8_t* sp = a.k_exp + row * 4 + g;
+      vs = *reinterpret_cast<const uint32_t*>(a.v_exp +
+                                              (vb * 4 + (n >> 2)) * (int64_t)a.page_size +
+                                              vsub * kUnit + 4 * (n & 3));
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         k[s] = *reinterpret_cast<const uint4*>(kp + s * (4 * kHeadDim / 2));
@@ -106,45 +127,56 @@ struct Cache4 {
       }
       const int half = a.page_size / 2;
       const uint8_t* vp =
-          a.v_cache + vb * (kHeadDim * (int64_t)half) + n * half + vsub * (kUnit / 2);
+          a.v_cache + vb * (kHeadDim * (int64_t)half) + 2 * n * half + vsub * (kUnit / 2);
+      if (a.page_size == kUnit) {  // two dims are 16 bytes
 #pragma unroll
-      for (int dt = 0; dt < 8; ++dt)
-        v[dt] = *reinterpret_cast<const uint2*>(vp + dt * 16 * half);
-      const uint8_t* ep = a.v_exp + vb * (4 * (int64_t)a.page_size) + vsub * kUnit;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vp + i * 32 * (kUnit / 2));
+          v[2 * i] = make_uint2(x.x, x.y);
+          v[2 * i + 1] = make_uint2(x.z, x.w);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        vs[i] = *reinterpret_cast<const uint4*>(ep + i * a.page_size);
-      top = *reinterpret_cast<const uint32_t*>(ep + (n >> 2) * a.page_size + 4 * (n & 3));
+        for (int i = 0; i < 8; ++i)
+          v[i] = *reinterpret_cast<const uint2*>(vp + ((i >> 1) * 32 + (i & 1)) * half);
+      }
     }
 
     template <int NT, int KIND, bool MIXED>
     __device__ __forceinline__ void add(AttnState<NT>& st, const at_bf16x8 (&q)[NT][4], int vblk,
                                         float call_scale, int pos, int have, const int (&len)[NT],
-                                        const float (&slope2)[NT], const Cap& cap, bool any) {
+                                        const float (&slope2)[NT], const Cap& cap, bool any,
+                                        Scratch& lds) {
       static_assert(!MIXED || NT == 1, "one visible length a lane");
-      // The unit's largest value scale, of the tokens that the row sees. NaN scales are
-      // left out of it, and make NaN of S.
-      bool nan = false;
-      uint32_t vtop = 0;
-      if (any) {
-        const int mine = min(have, len[0] - pos);
-        uint32_t bad = 0;
+      const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+      // The unit's largest value scale, of the tokens that the row sees, and the factors
+      // relative to it; NaN scales are left out (rows that see them are seen to below).
+      if (any) vs = keep_bytes(vs, have - 4 * (n & 3));
+      uint32_t vtop = group_top(vs);
+      const bool nan = __any(vtop == kNanScale);
+      if (nan) vtop = group_max(top_byte(vs));
+      // rows of different lengths that see a unit in part: each takes its own
+      const bool own = MIXED && any;
+      wave_order();  // (behind the loads of the tile before)
+      if (nan || own) reinterpret_cast<uint32_t*>(lds.bytes[g])[n] = vs;
+      const int mine = min(have, len[0] - pos);
+      if (own) {
+        wave_order();
+        vtop = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&vs[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w[j] = keep_bytes(w[j], mine - 4 * j);
-            vtop = max(vtop, top_byte(w[j]));
-            bad |= nan_scales(w[j]);
-          }
+          const uint4 w = lds.bytes[g][i];
+          vtop = max(max(vtop, max(top_byte(keep_bytes(w.x, mine)),
+                                   top_byte(keep_bytes(w.y, mine - 4)))),
+                     max(top_byte(keep_bytes(w.z, mine - 8)),
+                         top_byte(keep_bytes(w.w, mine - 12))));
         }
-        nan = __any(bad != 0);
-      } else {
-        vtop = group_max(top_byte(top));
-        nan = __any(nan_scales(top) != 0);
       }
       vtop = max(vtop, 15u);
+      const uint32_t floor2 = (vtop - 15u) * 0x00010001u;
+      if (!own)
+        lds.factor[g][n] = make_uint2(two_scales<0>(vs, floor2), two_scales<1>(vs, floor2));
+      wave_order();
       const float lv = (float)((int)vtop - 127);
       const float unlv = __uint_as_float((254u - vtop) << 23);
 
@@ -163,25 +195,27 @@ struct Cache4 {
             x[j][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kt, q[j][t], x[j][s], 0, 0, 0);
         }
       }
-      uint32_t p[NT][8];  // probabilities of token pairs, over 2^lv
+      uint32_t p[NT][8];  // probabilities of token pairs, times 2^lv
+      // (not 0 for masked scores)
+      const float sc = KIND != kPlain ? 1.f : fmaxf(call_scale, 0x1p-126f);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
+        if constexpr (KIND != kPlain) {
+          const float bias = -slope2[j] * (float)(len[j] - 1 - pos);
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            x[j][t >> 2][t & 3] = score2<KIND>(x[j][t >> 2][t & 3], call_scale, cap,
+                                               __builtin_fmaf((float)t, slope2[j], bias));
+        }
+        if (any) {
+          asm volatile("");  // a branch: few tiles are masked
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            if (t >= min(have, len[j] - pos)) x[j][t >> 2][t & 3] = -__builtin_inff();
+        }
         float best = -__builtin_inff();
-        const float bias = KIND == kPlain ? 0.f : -slope2[j] * (float)(len[j] - 1 - pos);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = 4 * s + i;
-            float y = x[j][s][i];
-            if constexpr (KIND != kPlain)
-              y = score2<KIND>(y, call_scale, cap, __builtin_fmaf((float)tok, slope2[j], bias));
-            if (any) y = (tok < have && pos + tok < len[j]) ? y : -__builtin_inff();
-            x[j][s][i] = y;
-            best = fmaxf(best, y);
-          }
-        // (not 0 for masked scores)
-        const float sc = KIND != kPlain ? 1.f : fmaxf(call_scale, 0x1p-126f);
+        for (int t = 0; t < 16; ++t) best = fmaxf(best, x[j][t >> 2][t & 3]);
         best = groups_max(__builtin_fmaf(best, sc, lv));
         if (__any(best > st.m[j] + kLazy)) {
           const float m = best > st.m[j] + kLazy ? best : st.m[j];
@@ -206,23 +240,24 @@ struct Cache4 {
         }
         st.l[j] = __builtin_fmaf(sum[0] + sum[1], unlv, st.l[j]);
       }
-      const uint32_t floor2 = (vtop - 15u) * 0x00010001u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {vs[i].x, vs[i].y, vs[i].z, vs[i].w};
         uint32_t sv[8];
+        if (own) {
+          asm volatile("");
+          const uint4 b = lds.bytes[g][i];
+          const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          sv[2 * t] = two_scales<0>(w[t], floor2);
-          sv[2 * t + 1] = two_scales<1>(w[t], floor2);
-        }
-        if (nan) {  // a rare path
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint32_t pair = w[t >> 1] >> (16 * (t & 1));
-            if ((pair & 255u) == kNanScale) sv[t] = (sv[t] & 0xFFFF0000u) | 0x7E00u;
-            if (((pair >> 8) & 255u) == kNanScale) sv[t] = (sv[t] & 0xFFFFu) | 0x7E000000u;
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t seen = keep_bytes(w[t], mine - 4 * t);
+            sv[2 * t] = two_scales<0>(seen, floor2);
+            sv[2 * t + 1] = two_scales<1>(seen, floor2);
           }
+        } else {
+          const uint4* f = reinterpret_cast<const uint4*>(&lds.factor[g][4 * i]);
+          const uint4 a = f[0], b = f[1];
+          sv[0] = a.x, sv[1] = a.y, sv[2] = a.z, sv[3] = a.w;
+          sv[4] = b.x, sv[5] = b.y, sv[6] = b.z, sv[7] = b.w;
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -239,6 +274,25 @@ struct Cache4 {
                                                                  st.o[j][dt], 0, 0, 0);
           }
         }
+      }
+      if (nan) {
+        // the groups of dims in which the row sees a NaN scale, of any unit
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = lds.bytes[g][i];
+          if ((nan_scales(keep_bytes(w.x, mine)) | nan_scales(keep_bytes(w.y, mine - 4)) |
+               nan_scales(keep_bytes(w.z, mine - 8)) | nan_scales(keep_bytes(w.w, mine - 12))) != 0)
+            bad |= 1u << i;
+        }
+        bad |= lane_xor<16>(bad);
+        bad |= lane_xor<32>(bad);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int dt = 0; dt < 8; ++dt)
+            if ((bad >> (dt >> 1)) & 1u)
+              st.o[j][dt] = at_f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
       }
     }
   };
@@ -258,6 +312,15 @@ struct Cache4 {
   template <int NT>
   static __device__ __forceinline__ void init(AttnState<NT>& st) {
     st.vref = 1.f;  // sums are in units of the reference alone
+  }
+  // (rows 4 g .. of the products 2 i and 2 i + 1 are the even and odd dims of eight)
+  static __device__ __forceinline__ int dim_of(int dt, int g) {
+    return 32 * (dt >> 1) + 8 * g + 4 * (dt & 1);
+  }
+  template <int NT>
+  static __device__ __forceinline__ at_f32x4 sums(const AttnState<NT>& st, int j, int dt) {
+    const at_f32x4 &a = st.o[j][dt & ~1], &b = st.o[j][dt | 1];
+    return dt & 1 ? at_f32x4{a[2], b[2], a[3], b[3]} : at_f32x4{a[0], b[0], a[1], b[1]};
   }
 };
 

@@ -2,7 +2,8 @@
 // cache's tiles (attend.hip: 8 bits, attend4.hip: 4 bits). A policy has
 //   load_query, init   a row's operand, and what a state starts with
 //   Tile               this lane's part of 64 tokens: load() asks for it, add() takes it
-//                      into a state
+//                      into a state, by way of a wave's Scratch in LDS
+//   dim_of, sums       the first dim of four, and the state's sums of them
 //
 // One token's query heads of one KV head are the 16 or 32 rows of the products (above 32
 // heads a group, two workgroups take 32 each); or, for prompt calls of few rows a request,
@@ -29,6 +30,7 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
   __shared__ int u_blk[kPhaseUnits], u_pos[kPhaseUnits];
   __shared__ float s_m[kAtWaves][16 * NT], s_l[kAtWaves][16 * NT];
   __shared__ __attribute__((aligned(16))) float s_o[16 * NT][kRowPad];
+  __shared__ typename Cache::Scratch scratch[kAtWaves];
 
   const int band = blockIdx.x % bands;  // of 16 NT query heads of the group
   const int h = blockIdx.x / bands % a.Hkv;
@@ -122,7 +124,8 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
       x.load(a, kblk, (u_pos[ku] & (a.page_size - 1)) / kUnit, vblk,
              (pos & (a.page_size - 1)) / kUnit, n, g);
       const bool any = !__all(have == kUnit && (!PACKED || pos + kUnit <= shortest));
-      x.template add<NT, KIND, PACKED>(st, q, vblk, call_scale, pos, have, len, slope2, cap, any);
+      x.template add<NT, KIND, PACKED>(st, q, vblk, call_scale, pos, have, len, slope2, cap, any,
+                                       scratch[w]);
     }
   }
 
@@ -150,8 +153,8 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int dt = 0; dt < 8; ++dt) {
-          at_f32x4* p = reinterpret_cast<at_f32x4*>(&s_o[16 * j + n][16 * dt + 4 * g]);
-          const at_f32x4 o = st.o[j][dt] * f[j];
+          at_f32x4* p = reinterpret_cast<at_f32x4*>(&s_o[16 * j + n][Cache::dim_of(dt, g)]);
+          const at_f32x4 o = Cache::sums(st, j, dt) * f[j];
           *p = i == 0 ? o : *p + o;
         }
     }
