@@ -29,7 +29,6 @@ namespace {
 constexpr int kP4Waves = 8;
 constexpr int kP4NT = kP4Waves * kWave;
 constexpr int kP4Rows = 32 * kP4Waves;
-constexpr int kP4PackedMean = 64;              // rows a request, up to which they are few
 constexpr int kP4CUs = 256;
 constexpr int kP4Phase = 512;                  // tiles whose pages wait in LDS
 constexpr int kP4Units = 4 * (kP4Phase + 4);   // and of the tiles loaded ahead
@@ -39,8 +38,9 @@ constexpr int kP4Frag = kWave;                 // uint4s of one operand in LDS
 struct Pre4Lds {
   uint4 k[2][16][kP4Frag];  // [buffer][32-token half, 16-dim step]
   uint4 v[2][16][kP4Frag];  // [buffer][32-dim tile, 32-token half, 8 tokens of the units]
-  uint4 scales[2][4][4];    // of the values: [buffer][unit][32 dims], a byte a token
-  uint32_t top[2][4];       // the units' largest
+  uint2 factor[2][4][16];   // of the values' scales: [buffer][unit][32 dims, four tokens]
+  uint4 scales[3][4][4];    // [buffer][unit][32 dims], a byte a token
+  uint32_t top[3][4];       // the units' largest
   int u_blk[kP4Units];
   int longest[kP4Waves], shortest[kP4Waves];
   unsigned long long work[kP4Waves];
@@ -51,23 +51,11 @@ __device__ __forceinline__ float p4_halves_max(float v) {
   return fmaxf(v, __uint_as_float(lane_xor<32>(__float_as_uint(v))));
 }
 
-// eight words of fp16 scales (token pairs of a unit) from its bytes of a group of dims
-__device__ __forceinline__ void unit_scales(uint4 bytes, uint32_t floor2, bool nan,
-                                            uint32_t (&s)[8]) {
-  const uint32_t w[4] = {bytes.x, bytes.y, bytes.z, bytes.w};
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    s[2 * t] = two_scales<0>(w[t], floor2);
-    s[2 * t + 1] = two_scales<1>(w[t], floor2);
-  }
-  if (nan) {
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const uint32_t pair = w[t >> 1] >> (16 * (t & 1));
-      if ((pair & 255u) == kNanScale) s[t] = (s[t] & 0xFFFF0000u) | 0x7E00u;
-      if (((pair >> 8) & 255u) == kNanScale) s[t] = (s[t] & 0xFFFFu) | 0x7E000000u;
-    }
-  }
+// NaN in the factors of NaN scales: two bytes of a word, their factors
+__device__ __forceinline__ uint32_t nan_factors(uint32_t pair, uint32_t s) {
+  if ((pair & 255u) == kNanScale) s = (s & 0xFFFF0000u) | 0x7E00u;
+  if (((pair >> 8) & 255u) == kNanScale) s = (s & 0xFFFFu) | 0x7E000000u;
+  return s;
 }
 
 // the bytes of the tokens that a row sees of 16
@@ -171,30 +159,44 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
   const int ktok = (tid & 7) | ((tid >> 6) << 3), kc = (tid >> 3) & 7;  // 8 tokens a wave
   const int ku = ktok >> 4;
   const int vd = tid & 127, vu = tid >> 7;
-  const int su = lane >> 4;  // this lane's unit, and word, of the values' scales
+  const uint8_t* k_at = a.k_cache + (ktok & 15) * (kHeadDim / 2) + 8 * kc;
+  const uint8_t* ks_at = a.k_exp + (ktok & 15) * 4 + (kc >> 1);
+  const uint8_t* v_at = a.v_cache + vd * hp;
+  const uint32_t block = (uint32_t)hp * kHeadDim, scales = (uint32_t)a.page_size * 4;
   uint2 kreg, vreg;
-  uint4 vscale;
-  uint32_t kscale, word;
+  uint32_t kscale, word = 0;
   auto load_k = [&](int c) {  // c: tile of the phase
     const int kb = lds.u_blk[4 * c + ku];
-    const int64_t at = (int64_t)max(kb, 0) * a.page_size +
-                       (((4 * (begin + c) + ku) & sub) * kUnit + (ktok & 15));
-    kreg = *reinterpret_cast<const uint2*>(a.k_cache + at * (kHeadDim / 2) + 8 * kc);
-    kscale = a.k_exp[at * 4 + (kc >> 1)];
+    const uint32_t s = (4 * (begin + c) + ku) & sub, at = (uint32_t)max(kb, 0);
+    kreg = *reinterpret_cast<const uint2*>(k_at + (uint64_t)at * block +
+                                           s * (kUnit * kHeadDim / 2));
+    kscale = ks_at[(uint64_t)at * scales + s * (kUnit * 4)];
     if (kb < 0) kreg = make_uint2(0, 0), kscale = 127;
   };
   auto load_v = [&](int c) {
-    const int vb = lds.u_blk[4 * c + vu], u = 4 * (begin + c) + vu;
-    vreg = *reinterpret_cast<const uint2*>(a.v_cache + (int64_t)max(vb, 0) * (kHeadDim * hp) +
-                                           (vd * hp + (u & sub) * (kUnit / 2)));
-    vscale = *reinterpret_cast<const uint4*>(
-        a.v_exp + ((int64_t)max(vb, 0) * 4 + (vd >> 5)) * a.page_size + (u & sub) * kUnit);
-    const int sb = lds.u_blk[4 * c + su], s = 4 * (begin + c) + su;
-    const uint32_t x = *reinterpret_cast<const uint32_t*>(
-        a.v_exp + ((int64_t)max(sb, 0) * 4 + ((lane >> 2) & 3)) * a.page_size +
-        (s & sub) * kUnit + 4 * (lane & 3));
-    if (vb < 0) vscale = make_uint4(0, 0, 0, 0);
-    word = sb < 0 ? 0u : x;
+    const int vb = lds.u_blk[4 * c + vu];
+    const uint32_t s = (4 * (begin + c) + vu) & sub;
+    vreg = *reinterpret_cast<const uint2*>(v_at + (uint64_t)(uint32_t)max(vb, 0) * block +
+                                           s * (kUnit / 2));
+  };
+  // The values' scales of a tile: one wave's, a tile ahead of the others' codes. A lane has
+  // unit lane / 16 and, of that, 32 dims (lane / 4 % 4) of four tokens.
+  auto load_scales = [&](int c) {
+    const int sb = lds.u_blk[4 * c + (lane >> 4)];
+    const uint32_t s = (4 * (begin + c) + (lane >> 4)) & sub;
+    word = *reinterpret_cast<const uint32_t*>(
+        a.v_exp + (uint64_t)(uint32_t)max(sb, 0) * scales + s * kUnit +
+        ((lane >> 2) & 3) * a.page_size + 4 * (lane & 3));
+    if (sb < 0) word = 0;
+  };
+  auto store_scales = [&](int c) {
+    const int su = lane >> 4, i = lane & 15, ring = (begin + c) % 3;
+    const uint32_t top = max(group_max(top_byte(word)), 15u), floor2 = (top - 15u) * 0x00010001u;
+    lds.factor[c & 1][su][i] =
+        make_uint2(nan_factors(word, two_scales<0>(word, floor2)),
+                   nan_factors(word >> 16, two_scales<1>(word, floor2)));
+    reinterpret_cast<uint32_t*>(lds.scales[ring][su])[i] = word;
+    if (i == 0) lds.top[ring][su] = top;
   };
   auto store_k = [&](int c) {
     // row 8 q + 4 (unit of the 32) + e holds token 4 q + e; every other step swaps rows 4
@@ -206,24 +208,17 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     p[32] = __builtin_bit_cast(uint4, codes4_bf16(kreg.y, s));
   };
   auto store_v = [&](int c) {
-    uint4 x[2] = {__builtin_bit_cast(uint4, codes4_f16(vreg.x)),
-                  __builtin_bit_cast(uint4, codes4_f16(vreg.y))};
-    if (in_part(c)) {
-      if (w == 0)
-        reinterpret_cast<uint32_t*>(&lds.scales[c & 1][su][(lane >> 2) & 3])[lane & 3] = word;
-    } else {
-      const uint32_t top = max(group_max(top_byte(word)), 15u);
-      const uint32_t mine = (uint32_t)__builtin_amdgcn_readlane((int)top, 16 * (w >> 1));
-      uint32_t s[8];
-      unit_scales(vscale, (mine - 15u) * 0x00010001u, __any(nan_scales(word) != 0), s);
-      uint32_t* y = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = mul_f16(y[i], s[i]);
-      if (w == 0 && (lane & 15) == 0) lds.top[c & 1][su] = top;
+    uint4 x = __builtin_bit_cast(uint4, codes4_f16(vreg.x));
+    uint4 y = __builtin_bit_cast(uint4, codes4_f16(vreg.y));
+    if (!in_part(c)) {
+      const uint4* f = reinterpret_cast<const uint4*>(&lds.factor[c & 1][vu][4 * (vd >> 5)]);
+      const uint4 s = f[0], t = f[1];
+      x = make_uint4(mul_f16(x.x, s.x), mul_f16(x.y, s.y), mul_f16(x.z, s.z), mul_f16(x.w, s.w));
+      y = make_uint4(mul_f16(y.x, t.x), mul_f16(y.y, t.y), mul_f16(y.z, t.z), mul_f16(y.w, t.w));
     }
     uint4* p = &lds.v[c & 1][((vd >> 5) * 2 + (vu >> 1)) * 2][(vu & 1) * 32 + (vd & 31)];
-    p[0] = x[0];
-    p[kP4Frag] = x[1];
+    p[0] = x;
+    p[kP4Frag] = y;
   };
 
   // the wave's state: sums in units of 2^m
@@ -264,6 +259,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     products(x, c);
     __builtin_amdgcn_sched_barrier(0);
     // maxima, masks and the reference
+    const int ring = (begin + c) % 3;
     int have[2];
     uint32_t top[2];
     float lv[2];
@@ -275,13 +271,13 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       const int i = 4 * c + 2 * ts + half, pos = (4 * begin + i) * kUnit;
       have[ts] = lds.u_blk[i] < 0 ? 0 : min(kUnit, len - pos);
       if constexpr (!part) {
-        top[ts] = lds.top[c & 1][2 * ts + half];
+        top[ts] = lds.top[ring][2 * ts + half];
       } else {
         uint32_t bad = 0;
         top[ts] = 15u;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const uint4 s = seen_bytes(lds.scales[c & 1][2 * ts + half][d], have[ts]);
+          const uint4 s = seen_bytes(lds.scales[ring][2 * ts + half][d], have[ts]);
           top[ts] = max(max(max(top[ts], top_byte(s.x)), max(top_byte(s.y), top_byte(s.z))),
                         top_byte(s.w));
           bad |= nan_scales(s.x) | nan_scales(s.y) | nan_scales(s.z) | nan_scales(s.w);
@@ -365,9 +361,19 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       for (int ts = 0; ts < 2; ++ts) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
+          const uint4 b = seen_bytes(lds.scales[ring][2 * ts + half][d], have[ts]);
+          const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, floor2 = (top[ts] - 15u) * 0x00010001u;
           uint32_t s[8];
-          unit_scales(seen_bytes(lds.scales[c & 1][2 * ts + half][d], have[ts]),
-                      (top[ts] - 15u) * 0x00010001u, nan, s);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[2 * e] = two_scales<0>(bw[e], floor2);
+            s[2 * e + 1] = two_scales<1>(bw[e], floor2);
+            if (nan) {
+              asm volatile("");  // a branch: rare
+              s[2 * e] = nan_factors(bw[e], s[2 * e]);
+              s[2 * e + 1] = nan_factors(bw[e] >> 16, s[2 * e + 1]);
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint4 y = p[2 * ts + e];
@@ -395,9 +401,12 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       lds.u_blk[i] = i < 4 * count && u < units ? block_of(a, pages, u >> ush, h) : -1;
     }
     __syncthreads();
+    if (w < 3) load_scales(w);
     load_k(0);
     load_v(0);
+    if (w < 2) store_scales(w);
     store_k(0);
+    __syncthreads();
     store_v(0);
     load_k(1);
     load_v(1);
@@ -409,6 +418,8 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
         store_v(c + 1);
         load_k(c + 2);
         load_v(c + 2);
+        if (w == ((c + 2) & 7)) store_scales(c + 2);
+        if (w == ((c + 3) & 7)) load_scales(c + 3);
       }
     };
     const int whole = (int)min((int64_t)count, max((int64_t)least / kTileTok - begin, (int64_t)0));
