@@ -62,8 +62,10 @@ struct Cache8 {
 };
 
 // The splits' sums of one (row, query head), each in units of its own maximum: TEAMS
-// teams of 32 lanes, four dims a lane, take every TEAMS-th split, four at a time with
-// their loads in flight, and are joined in LDS. Fixed orders: the same sums every time.
+// teams of 32 lanes, four dims a lane, take every TEAMS-th split, four at a time, and are
+// joined in LDS. Fixed orders: the same sums every time. Short: a launch and chains of loads
+// (64 splits of 128 items: MERGE_US us with eight splits' loads in flight, 5.7 with the sums
+// behind the weights of four).
 template <int TEAMS>
 __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t items,
                                                              int splits) {
@@ -82,39 +84,39 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
   float m = -__builtin_inff(), l = 0.f;
   at_f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
-    constexpr int kStep = 4;
-    for (int s0 = team; s0 < splits; s0 += kStep * TEAMS) {
-      at_f32x2 ml[kStep];
-      at_f32x4 x[kStep];
+    // (loads of kLoads steps of kStep splits are in flight at once; a split without tokens
+    // has no weight: its sums are not taken, whatever they hold)
+    constexpr int kStep = 4, kLoads = 2;
+    for (int s0 = team; s0 < splits; s0 += kLoads * kStep * TEAMS) {
+      at_f32x2 ml[kLoads * kStep];
+      at_f32x4 x[kLoads * kStep];
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        const int s = s0 + i * TEAMS;
-        const int64_t p = first + (int64_t)min(s, splits - 1) * G;
+      for (int i = 0; i < kLoads * kStep; ++i) {
+        const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
         ml[i] = *reinterpret_cast<const at_f32x2*>(a.part_ml + 2 * p);
-        if (s >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
+        x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
       }
-      // (a split without tokens has no weight: its sums, zeros, need not be read)
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};
-        if (ml[i][1] != 0.f) {
-          const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
-          x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
+      for (int i = 0; i < kLoads * kStep; ++i) {
+        if (s0 + i * TEAMS >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
+        if (ml[i][1] == 0.f) x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads * kStep; j += kStep) {
+        float top = m;
+#pragma unroll
+        for (int i = j; i < j + kStep; ++i) top = fmaxf(top, ml[i][0]);
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        const float f = exp2_fast(m - base);
+        m = top;
+        l *= f;
+        o *= f;
+#pragma unroll
+        for (int i = j; i < j + kStep; ++i) {
+          const float w = exp2_fast(ml[i][0] - base);
+          l += ml[i][1] * w;
+          o += x[i] * w;
         }
-      }
-      float top = m;
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) top = fmaxf(top, ml[i][0]);
-      const float base = top == -__builtin_inff() ? 0.f : top;
-      const float f = exp2_fast(m - base);
-      m = top;
-      l *= f;
-      o *= f;
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        const float w = exp2_fast(ml[i][0] - base);
-        l += ml[i][1] * w;
-        o += x[i] * w;
       }
     }
   }
