@@ -15,6 +15,9 @@ namespace {
 // A lane's part of a tile: its key bytes (unit n / 4), value bytes (unit g) and that unit's
 // scales.
 struct Cache8 {
+  static constexpr bool kRowsInLds = false;
+  template <int NT, int KIND, bool PACKED>
+  static constexpr int kWaves = 2;
   struct Scratch {};
   struct Tile {
     uint4 k[4][2], v[8];
@@ -54,6 +57,11 @@ struct Cache8 {
   }
   template <int NT>
   static __device__ __forceinline__ void init(AttnState<NT>&) {}
+  template <int NT>
+  static __device__ __forceinline__ const at_bf16x8 (&rows(const at_bf16x8 (&q)[NT][4],
+                                                           const uint4 (&)[1][kWave]))[NT][4] {
+    return q;
+  }
   static __device__ __forceinline__ int dim_of(int dt, int g) { return 16 * dt + 4 * g; }
   template <int NT>
   static __device__ __forceinline__ at_f32x4 sums(const AttnState<NT>& st, int j, int dt) {
@@ -64,8 +72,8 @@ struct Cache8 {
 // The splits' sums of one (row, query head), each in units of its own maximum: TEAMS
 // teams of 32 lanes, four dims a lane, take every TEAMS-th split, four at a time, and are
 // joined in LDS. Fixed orders: the same sums every time. Short: a launch and chains of loads
-// (64 splits of 128 items: MERGE_US us with eight splits' loads in flight, 5.7 with the sums
-// behind the weights of four).
+// (64 splits of 128 items: 4.9 us with eight splits' loads in flight, 5.7 with the sums behind
+// the weights of four).
 template <int TEAMS>
 __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t items,
                                                              int splits) {
@@ -84,9 +92,9 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
   float m = -__builtin_inff(), l = 0.f;
   at_f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
-    // (loads of kLoads steps of kStep splits are in flight at once; a split without tokens
-    // has no weight: its sums are not taken, whatever they hold)
-    constexpr int kStep = 4, kLoads = 2;
+    // A split without tokens has no weight: its sums are not taken, whatever they hold. Few
+    // items ask for two steps' weights and sums at once, many save those splits' bytes.
+    constexpr int kStep = 4, kLoads = TEAMS == 8 ? 2 : 1;
     for (int s0 = team; s0 < splits; s0 += kLoads * kStep * TEAMS) {
       at_f32x2 ml[kLoads * kStep];
       at_f32x4 x[kLoads * kStep];
@@ -94,12 +102,18 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
       for (int i = 0; i < kLoads * kStep; ++i) {
         const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
         ml[i] = *reinterpret_cast<const at_f32x2*>(a.part_ml + 2 * p);
-        x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
+        if (TEAMS == 8)
+          x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
+        if (s0 + i * TEAMS >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
       }
 #pragma unroll
       for (int i = 0; i < kLoads * kStep; ++i) {
-        if (s0 + i * TEAMS >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
-        if (ml[i][1] == 0.f) x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};
+        if (ml[i][1] == 0.f) {
+          x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};
+        } else if (TEAMS != 8) {
+          const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
+          x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
+        }
       }
 #pragma unroll
       for (int j = 0; j < kLoads * kStep; j += kStep) {

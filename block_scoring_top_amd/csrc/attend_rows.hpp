@@ -4,6 +4,9 @@
 //   Tile               this lane's part of 64 tokens: load() asks for it, add() takes it
 //                      into a state, by way of a wave's Scratch in LDS
 //   dim_of, sums       the first dim of four, and the state's sums of them
+//   kRowsInLds, rows   where add() finds the rows' operands: registers, or LDS, which all
+//                      waves share
+//   kWaves             waves a SIMD that an instance's registers are cut to
 //
 // One token's query heads of one KV head are the 16 or 32 rows of the products (above 32
 // heads a group, two workgroups take 32 each); or, for prompt calls of few rows a request,
@@ -25,12 +28,13 @@ constexpr int kPhaseUnits = 4 * kPhase;
 constexpr int kRowPad = kHeadDim + 4;         // floats of a row of sums in LDS
 
 template <class Cache, int NT, int KIND, bool PACKED>
-__global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int chunk, int splits,
-                                                               int bands) {
+__global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) void attend_rows_kernel(
+    AttnArgs a, int chunk, int splits, int bands) {
   __shared__ int u_blk[kPhaseUnits], u_pos[kPhaseUnits];
   __shared__ float s_m[kAtWaves][16 * NT], s_l[kAtWaves][16 * NT];
   __shared__ __attribute__((aligned(16))) float s_o[16 * NT][kRowPad];
   __shared__ typename Cache::Scratch scratch[kAtWaves];
+  __shared__ uint4 s_q[Cache::kRowsInLds ? 4 * NT : 1][kWave];
 
   const int band = blockIdx.x % bands;  // of 16 NT query heads of the group
   const int h = blockIdx.x / bands % a.Hkv;
@@ -86,6 +90,12 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
       shortest = min(shortest, __shfl_xor(shortest, d));
     }
   }
+  if (Cache::kRowsInLds && w == 0) {  // (the waves meet at the first phase)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_q[4 * j + i][lane] = __builtin_bit_cast(uint4, q[j][i]);
+  }
   AttnState<NT> st;
   attn_init(st);
   Cache::init(st);
@@ -124,8 +134,8 @@ __global__ __launch_bounds__(kAtNT, 2) void attend_rows_kernel(AttnArgs a, int c
       x.load(a, kblk, (u_pos[ku] & (a.page_size - 1)) / kUnit, vblk,
              (pos & (a.page_size - 1)) / kUnit, n, g);
       const bool any = !__all(have == kUnit && (!PACKED || pos + kUnit <= shortest));
-      x.template add<NT, KIND, PACKED>(st, q, vblk, call_scale, pos, have, len, slope2, cap, any,
-                                       scratch[w]);
+      x.template add<NT, KIND, PACKED>(st, Cache::rows(q, s_q), vblk, call_scale, pos, have, len,
+                                       slope2, cap, any, scratch[w]);
     }
   }
 
