@@ -73,13 +73,55 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int have) {
 }
 
 // Two scales (bytes 2 i, 2 i + 1 of w) as fp16 relative to the scale byte floor + 15:
-// 2^(byte - floor - 15), zero from 2^-15 on. Bytes are at most floor + 15.
-template <int I>
+// 2^(byte - floor - 15), zero from 2^-15 on. Bytes are at most floor + 15, or, with CLAMP,
+// larger ones (of tokens that a row does not see, or NaN) give something finite.
+template <int I, bool CLAMP = false>
 __device__ __forceinline__ uint32_t two_scales(uint32_t w, uint32_t floor2) {
   const uint32_t b = __builtin_amdgcn_perm(0u, w, I == 0 ? 0x0C010C00u : 0x0C030C02u);
-  const at_u16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(at_u16x2, b),
-                                                   __builtin_bit_cast(at_u16x2, floor2));
+  at_u16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(at_u16x2, b),
+                                             __builtin_bit_cast(at_u16x2, floor2));
+  if constexpr (CLAMP) d = __builtin_elementwise_min(d, at_u16x2{30, 30});
   return __builtin_bit_cast(uint32_t, d << (uint16_t)10);
+}
+// bytes of two words, the larger of each place
+__device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(at_u16x2, a),
+                                                                __builtin_bit_cast(at_u16x2, b)));
+}
+constexpr uint32_t kEvenBytes = 0x00FF00FFu;
+// A group's 16 lanes hold, each, a byte for four tokens, of four blocks of 32 dims (lane i:
+// block i / 4, tokens 4 (i % 4) ..): the largest of each token, NaN left out, in every lane of
+// its place.
+__device__ __forceinline__ uint32_t token_tops(uint32_t w) {
+  w &= ~((nan_scales(w) >> 7) * 255u);
+  uint32_t even = w & kEvenBytes, odd = (w >> 8) & kEvenBytes;
+  even = max_u16(even, dpp_u32<kDppRowRor1 + 3>(even));
+  odd = max_u16(odd, dpp_u32<kDppRowRor1 + 3>(odd));
+  even = max_u16(even, dpp_u32<kDppRowRor1 + 7>(even));
+  odd = max_u16(odd, dpp_u32<kDppRowRor1 + 7>(odd));
+  return even | (odd << 8);
+}
+// the largest of 16 tokens' bytes, of the first `have`
+__device__ __forceinline__ uint32_t seen_top(uint4 tops, int have) {
+  const uint32_t w[4] = {keep_bytes(tops.x, have), keep_bytes(tops.y, have - 4),
+                         keep_bytes(tops.z, have - 8), keep_bytes(tops.w, have - 12)};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = max_u16(m, max_u16(w[i] & kEvenBytes, (w[i] >> 8) & kEvenBytes));
+  return max(m & 0xFFFFu, m >> 16);
+}
+// which of the four blocks of dims hold a NaN scale of the first `have` tokens
+__device__ __forceinline__ uint32_t seen_nans(const uint4 (&bytes)[4], int have) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = bytes[i];
+    if ((nan_scales(keep_bytes(w.x, have)) | nan_scales(keep_bytes(w.y, have - 4)) |
+         nan_scales(keep_bytes(w.z, have - 8)) | nan_scales(keep_bytes(w.w, have - 12))) != 0)
+      bad |= 1u << i;
+  }
+  return bad;
 }
 __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(at_f16x2, a) *
@@ -109,6 +151,7 @@ struct Cache4 {
   // word of four tokens each, read by all of them.
   struct Scratch {
     uint4 bytes[4][4];    // [unit][32 dims], a byte a token
+    uint32_t tops[4][4];  // [unit], a byte a token: its largest
     uint2 factor[4][16];  // [unit][32 dims, four tokens]
   };
   struct Tile {
@@ -167,16 +210,9 @@ struct Cache4 {
       if (nan || own) reinterpret_cast<uint32_t*>(lds.bytes[g])[n] = vs;
       const int mine = min(have, len[0] - pos);
       if (own) {
+        lds.tops[g][n & 3] = token_tops(vs);
         wave_order();
-        vtop = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = lds.bytes[g][i];
-          vtop = max(max(vtop, max(top_byte(keep_bytes(w.x, mine)),
-                                   top_byte(keep_bytes(w.y, mine - 4)))),
-                     max(top_byte(keep_bytes(w.z, mine - 8)),
-                         top_byte(keep_bytes(w.w, mine - 12))));
-        }
+        vtop = seen_top(*reinterpret_cast<const uint4*>(lds.tops[g]), mine);
       }
       vtop = max(vtop, 15u);
       const uint32_t floor2 = (vtop - 15u) * 0x00010001u;
@@ -256,9 +292,8 @@ struct Cache4 {
           const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const uint32_t seen = keep_bytes(w[t], mine - 4 * t);
-            sv[2 * t] = two_scales<0>(seen, floor2);
-            sv[2 * t + 1] = two_scales<1>(seen, floor2);
+            sv[2 * t] = two_scales<0, true>(w[t], floor2);
+            sv[2 * t + 1] = two_scales<1, true>(w[t], floor2);
           }
         } else {
           const uint4* f = reinterpret_cast<const uint4*>(&lds.factor[g][4 * i]);
@@ -284,14 +319,7 @@ struct Cache4 {
       }
       if (nan) {
         // the groups of dims in which the row sees a NaN scale, of any unit
-        uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = lds.bytes[g][i];
-          if ((nan_scales(keep_bytes(w.x, mine)) | nan_scales(keep_bytes(w.y, mine - 4)) |
-               nan_scales(keep_bytes(w.z, mine - 8)) | nan_scales(keep_bytes(w.w, mine - 12))) != 0)
-            bad |= 1u << i;
-        }
+        uint32_t bad = seen_nans(lds.bytes[g], mine);
         bad |= lane_xor<16>(bad);
         bad |= lane_xor<32>(bad);
 #pragma unroll

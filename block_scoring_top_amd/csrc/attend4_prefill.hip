@@ -40,7 +40,9 @@ struct Pre4Lds {
   uint4 v[2][16][kP4Frag];  // [buffer][32-dim tile, 32-token half, 8 tokens of the units]
   uint2 factor[2][4][16];   // of the values' scales: [buffer][unit][32 dims, four tokens]
   uint4 scales[3][4][4];    // [buffer][unit][32 dims], a byte a token
+  uint4 tops[3][4];         // each token's largest, a byte
   uint32_t top[3][4];       // the units' largest
+  int nan_tile[3];          // a tile with NaN scales (plus one)
   int u_blk[kP4Units];
   int longest[kP4Waves], shortest[kP4Waves];
   unsigned long long work[kP4Waves];
@@ -56,12 +58,6 @@ __device__ __forceinline__ uint32_t nan_factors(uint32_t pair, uint32_t s) {
   if ((pair & 255u) == kNanScale) s = (s & 0xFFFF0000u) | 0x7E00u;
   if (((pair >> 8) & 255u) == kNanScale) s = (s & 0xFFFFu) | 0x7E000000u;
   return s;
-}
-
-// the bytes of the tokens that a row sees of 16
-__device__ __forceinline__ uint4 seen_bytes(uint4 w, int have) {
-  return make_uint4(keep_bytes(w.x, have), keep_bytes(w.y, have - 4), keep_bytes(w.z, have - 8),
-                    keep_bytes(w.w, have - 12));
 }
 
 template <int KIND>
@@ -191,12 +187,16 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
   };
   auto store_scales = [&](int c) {
     const int su = lane >> 4, i = lane & 15, ring = (begin + c) % 3;
-    const uint32_t top = max(group_max(top_byte(word)), 15u), floor2 = (top - 15u) * 0x00010001u;
+    const uint32_t tops = token_tops(word);
+    const uint32_t top = max(group_top(tops), 15u), floor2 = (top - 15u) * 0x00010001u;
     lds.factor[c & 1][su][i] =
         make_uint2(nan_factors(word, two_scales<0>(word, floor2)),
                    nan_factors(word >> 16, two_scales<1>(word, floor2)));
     reinterpret_cast<uint32_t*>(lds.scales[ring][su])[i] = word;
+    if (i < 4) reinterpret_cast<uint32_t*>(&lds.tops[ring][su])[i] = tops;
     if (i == 0) lds.top[ring][su] = top;
+    const bool nan = __any(nan_scales(word) != 0);
+    if (lane == 0) lds.nan_tile[ring] = nan ? begin + c + 1 : 0;
   };
   auto store_k = [&](int c) {
     // row 8 q + 4 (unit of the 32) + e holds token 4 q + e; every other step swaps rows 4
@@ -263,7 +263,6 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     int have[2];
     uint32_t top[2];
     float lv[2];
-    bool nan = false;
     float best = -__builtin_inff();
     const float sc = KIND != kPlain ? 1.f : fmaxf(call_scale, 0x1p-126f);
 #pragma unroll
@@ -273,17 +272,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       if constexpr (!part) {
         top[ts] = lds.top[ring][2 * ts + half];
       } else {
-        uint32_t bad = 0;
-        top[ts] = 15u;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint4 s = seen_bytes(lds.scales[ring][2 * ts + half][d], have[ts]);
-          top[ts] = max(max(max(top[ts], top_byte(s.x)), max(top_byte(s.y), top_byte(s.z))),
-                        top_byte(s.w));
-          bad |= nan_scales(s.x) | nan_scales(s.y) | nan_scales(s.z) | nan_scales(s.w);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        nan |= __any(bad != 0);
+        top[ts] = max(seen_top(lds.tops[ring][2 * ts + half], have[ts]), 15u);
       }
       lv[ts] = (float)((int)top[ts] - 127);
       if constexpr (KIND != kPlain) {
@@ -361,18 +350,13 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       for (int ts = 0; ts < 2; ++ts) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const uint4 b = seen_bytes(lds.scales[ring][2 * ts + half][d], have[ts]);
+          const uint4 b = lds.scales[ring][2 * ts + half][d];
           const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, floor2 = (top[ts] - 15u) * 0x00010001u;
           uint32_t s[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[2 * e] = two_scales<0>(bw[e], floor2);
-            s[2 * e + 1] = two_scales<1>(bw[e], floor2);
-            if (nan) {
-              asm volatile("");  // a branch: rare
-              s[2 * e] = nan_factors(bw[e], s[2 * e]);
-              s[2 * e + 1] = nan_factors(bw[e] >> 16, s[2 * e + 1]);
-            }
+            s[2 * e] = two_scales<0, true>(bw[e], floor2);
+            s[2 * e + 1] = two_scales<1, true>(bw[e], floor2);
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -384,6 +368,19 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
           }
           __builtin_amdgcn_sched_barrier(0);  // few tiles: no registers for it
         }
+      }
+      if (lds.nan_tile[ring] == begin + c + 1) {
+        // the groups of dims in which the row sees a NaN scale
+        uint32_t bad = 0;
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+          bad |= seen_nans(lds.scales[ring][2 * ts + half], have[ts]);
+        bad |= lane_xor<32>(bad);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if ((bad >> d) & 1u) o[d][i] = __builtin_nanf("");
       }
     }
     __builtin_amdgcn_sched_barrier(0);
