@@ -13,6 +13,17 @@
 //     reaches just the rows that see it.
 //   - The reference of a row's sums is the running maximum of score + lv, moved when it has
 //     grown by 2^kLazy or more.
+// Two prompts of 8009 and 8192 tokens, 32 heads on 8: 1.12 ms, 0.96 PFLOP/s (a large library
+// product reaches 1.21 on this card). Bound by the products and the exponentials beside them
+// at the clock that the card holds under both. What led there: 2.93 ms with 16 rows a product
+// straight from the cache; 1.24 as described; 1.21 with the scales' factors made by one wave
+// a tile instead of each thread's own; 1.17 with the tokens' largest scales found once and
+// factors of unseen tokens clamped, not masked (the tiles at the rows' ends took four times
+// the others' time); 1.13 with the next tile stored before this one's products, not behind
+// them; 1.12 with the exponentials at a higher priority than products (the products there
+// instead: 1.13). Scores from products of the codes themselves (the block-scaled matrix
+// instructions, a query as two e4m3 parts) were measured apart: off by up to 2^-17 of
+// sum |q k|, 2^-13 where a key's scales lie 2^12 apart, and not built.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -258,6 +269,8 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     at_f32x16 x[2];
     products(x, c);
     __builtin_amdgcn_sched_barrier(0);
+    // (a SIMD's other wave, at its products, gives way to the exponentials of this one)
+    __builtin_amdgcn_s_setprio(1);
     // maxima, masks and the reference
     const int ring = (begin + c) % 3;
     int have[2];
@@ -333,6 +346,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       p[2 * ts + 1] = make_uint4(wd[4], wd[5], wd[6], wd[7]);
     }
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
     if constexpr (!part) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -410,11 +424,12 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     auto tiles = [&](int from, int to, auto part_of) {
       for (int c = from; c < to; ++c) {
         __syncthreads();  // tile c is written, tile c - 1 read
-        if (c < mine) step(c, part_of);
+        // (the next tile first: its loads have had a step's time, the one after gets one)
         store_k(c + 1);
         store_v(c + 1);
         load_k(c + 2);
         load_v(c + 2);
+        if (c < mine) step(c, part_of);
         if (w == ((c + 2) & 7)) store_scales(c + 2);
         if (w == ((c + 3) & 7)) load_scales(c + 3);
       }
