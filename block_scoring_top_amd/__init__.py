@@ -683,9 +683,9 @@ def _cache4(dev, k_cache, v_cache, k_scale, v_scale):
             raise ValueError("all tensors must live on the same GPU")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-    if not (k_cache.dtype is v_cache.dtype and k_cache.dtype in (_BYTE, _E2M1)):
+    if not (k_cache.dtype is v_cache.dtype is _BYTE or k_cache.dtype is v_cache.dtype is _E2M1):
         raise TypeError("the caches must be uint8 (two codes a byte) or float4_e2m1fn_x2")
-    if not (k_scale.dtype is v_scale.dtype and k_scale.dtype in (_BYTE, _E8M0)):
+    if not (k_scale.dtype is v_scale.dtype is _BYTE or k_scale.dtype is v_scale.dtype is _E8M0):
         raise TypeError("the scales must be uint8 or float8_e8m0fnu")
     n_pages, Hkv, page, half = k_cache.shape
     D = 2 * half
@@ -727,19 +727,25 @@ def idx_cache4_read(slots, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloa
     dev = _gpu(k_cache)
     n_pages, Hkv, page, D = _cache4(dev, k_cache, v_cache, k_scale, v_scale)
     _words(dev, slots)
-    shape = (slots.numel(), Hkv, D)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=dev)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=dev)
-    ks, vs = _rows("k_out", k_out, dev), _rows("v_out", v_out, dev)
-    if not k_out.shape == v_out.shape == shape or k_out.dtype is not v_out.dtype:
-        raise ValueError("k_out and v_out must be [slots, Hkv, D] of one dtype")
-    if k_out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {k_out.dtype}")
+    n = slots.numel()
+    if k_out is None and v_out is None:
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise TypeError(f"unsupported dtype {dtype}")
+        k_out, v_out = torch.empty(2, n, Hkv, D, dtype=dtype, device=dev).unbind(0)
+        ks = vs = Hkv * D
+    else:
+        if k_out is None:
+            k_out = torch.empty(n, Hkv, D, dtype=v_out.dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty(n, Hkv, D, dtype=k_out.dtype, device=dev)
+        ks, vs = _rows("k_out", k_out, dev), _rows("v_out", v_out, dev)
+        if not k_out.shape == v_out.shape == (n, Hkv, D) or k_out.dtype is not v_out.dtype:
+            raise ValueError("k_out and v_out must be [slots, Hkv, D] of one dtype")
+        if k_out.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"unsupported dtype {k_out.dtype}")
     _launch("idx_cache4_read", dev, lib.idx_cache4_read, slots.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_out.data_ptr(),
-            v_out.data_ptr(), ks, vs, shape[0], Hkv, D, n_pages, page, _dtype_code(k_out))
+            v_out.data_ptr(), ks, vs, n, Hkv, D, n_pages, page, _dtype_code(k_out))
     return k_out, v_out
 
 
@@ -801,8 +807,9 @@ def idx_rope_table(rot, base=10000.0, kind="plain", stretch=1.0, original=8192.0
 def _rope_out(name, x, out, dev):
     """An output of idx_rope (a new one by default), and its row stride."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype is not x.dtype:
+        n, heads, D = x.shape
+        return torch.empty(n, heads, D, dtype=x.dtype, device=dev), heads * D
+    if out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError(f"{name} must have its input's shape and dtype")
     return out, _rows(name, out, dev)
 
@@ -820,20 +827,21 @@ def idx_rope(q, k, tok_len, turns, first=0, interleaved=False, inverse=False, fa
     dev = _gpu(q)
     qs = _rows("q", q, dev)
     n, Hq, D = q.shape
+    dtype = q.dtype
     _words(dev, tok_len)
     if tok_len.numel() != n:
         raise ValueError("tok_len must hold one entry per row of q")
     if (turns.device != dev or turns.dtype is not torch.int64 or turns.dim() != 1
             or not turns.is_contiguous()):
         raise ValueError("turns must be a row of int64 on q's GPU")
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {q.dtype}")
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"unsupported dtype {dtype}")
     q_out, qos = _rope_out("q_out", q, q_out, dev)
     Hkv, ks, kos, kp, kop = 0, 0, 0, None, None
     if k is not None:
         ks = _rows("k", k, dev)
         Hkv = k.shape[1]
-        if k.shape != (n, Hkv, D) or k.dtype is not q.dtype:
+        if k.shape != (n, Hkv, D) or k.dtype is not dtype:
             raise ValueError("k must be [rows of q, Hkv, D] of q's dtype")
         k_out, kos = _rope_out("k_out", k, k_out, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -842,7 +850,7 @@ def idx_rope(q, k, tok_len, turns, first=0, interleaved=False, inverse=False, fa
     flags = (IDX_ROPE_ADJACENT if interleaved else 0) | (IDX_ROPE_INVERSE if inverse else 0)
     _launch("idx_rope", dev, lib.idx_rope, q.data_ptr(), kp, qs, ks, tok_len.data_ptr(),
             turns.data_ptr(), q_out.data_ptr(), kop, qos, kos, n, Hq, Hkv, D, first,
-            2 * turns.numel(), factor, flags, _dtype_code(q))
+            2 * turns.numel(), factor, flags, IDX_BF16 if dtype is torch.bfloat16 else IDX_F32)
     return q_out, k_out
 
 
