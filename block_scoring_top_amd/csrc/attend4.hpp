@@ -72,21 +72,27 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int have) {
   return have >= 4 ? w : have <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * have));
 }
 
-// Two scales (bytes 2 i, 2 i + 1 of w) as fp16 relative to the scale byte floor + 15:
-// 2^(byte - floor - 15), zero from 2^-15 on. Bytes are at most floor + 15, or, with CLAMP,
-// larger ones (of tokens that a row does not see, or NaN) give something finite.
-template <int I, bool CLAMP = false>
-__device__ __forceinline__ uint32_t two_scales(uint32_t w, uint32_t floor2) {
-  const uint32_t b = __builtin_amdgcn_perm(0u, w, I == 0 ? 0x0C010C00u : 0x0C030C02u);
-  at_u16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(at_u16x2, b),
-                                             __builtin_bit_cast(at_u16x2, floor2));
-  if constexpr (CLAMP) d = __builtin_elementwise_min(d, at_u16x2{30, 30});
-  return __builtin_bit_cast(uint32_t, d << (uint16_t)10);
-}
 // bytes of two words, the larger of each place
 __device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(at_u16x2, a),
                                                                 __builtin_bit_cast(at_u16x2, b)));
+}
+// Two scales (bytes 2 i, 2 i + 1 of w) as fp16 relative to the scale byte floor + 25:
+// 2^(byte - floor - 25), down to the least subnormal, 2^-24; zero from 2^-25 on. Bytes are at
+// most floor + 25, or, with CLAMP, larger ones (of tokens that a row does not see, or NaN) give
+// something finite. (Bit patterns are in the order of the values: e = byte - floor above 10 has
+// the exponent e - 10, the others are 2^(e - 1) units of 2^-24.)
+constexpr uint32_t kBelow = 25;
+template <int I, bool CLAMP = false>
+__device__ __forceinline__ uint32_t two_scales(uint32_t w, uint32_t floor2) {
+  const uint32_t b = __builtin_amdgcn_perm(0u, w, I == 0 ? 0x0C010C00u : 0x0C030C02u);
+  at_u16x2 e = __builtin_elementwise_sub_sat(__builtin_bit_cast(at_u16x2, b),
+                                             __builtin_bit_cast(at_u16x2, floor2));
+  if constexpr (CLAMP) e = __builtin_elementwise_min(e, at_u16x2{40, 40});
+  const at_u16x2 normal = __builtin_elementwise_sub_sat(e, at_u16x2{10, 10}) << (uint16_t)10;
+  const at_u16x2 small = (at_u16x2{1, 1} << __builtin_elementwise_min(e, at_u16x2{10, 10})) >>
+                         (uint16_t)1;
+  return max_u16(__builtin_bit_cast(uint32_t, normal), __builtin_bit_cast(uint32_t, small));
 }
 constexpr uint32_t kEvenBytes = 0x00FF00FFu;
 // A group's 16 lanes hold, each, a byte for four tokens, of four blocks of 32 dims (lane i:
@@ -214,8 +220,8 @@ struct Cache4 {
         wave_order();
         vtop = seen_top(*reinterpret_cast<const uint4*>(lds.tops[g]), mine);
       }
-      vtop = max(vtop, 15u);
-      const uint32_t floor2 = (vtop - 15u) * 0x00010001u;
+      vtop = max(vtop, kBelow);
+      const uint32_t floor2 = (vtop - kBelow) * 0x00010001u;
       if (!own)
         lds.factor[g][n] = make_uint2(two_scales<0>(vs, floor2), two_scales<1>(vs, floor2));
       wave_order();

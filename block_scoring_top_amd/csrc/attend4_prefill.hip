@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
   auto store_scales = [&](int c) {
     const int su = lane >> 4, i = lane & 15, ring = (begin + c) % 3;
     const uint32_t tops = token_tops(word);
-    const uint32_t top = max(group_top(tops), 15u), floor2 = (top - 15u) * 0x00010001u;
+    const uint32_t top = max(group_top(tops), kBelow), floor2 = (top - kBelow) * 0x00010001u;
     lds.factor[c & 1][su][i] =
         make_uint2(nan_factors(word, two_scales<0>(word, floor2)),
                    nan_factors(word >> 16, two_scales<1>(word, floor2)));
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
       if constexpr (!part) {
         top[ts] = lds.top[ring][2 * ts + half];
       } else {
-        top[ts] = max(seen_top(lds.tops[ring][2 * ts + half], have[ts]), 15u);
+        top[ts] = max(seen_top(lds.tops[ring][2 * ts + half], have[ts]), kBelow);
       }
       lv[ts] = (float)((int)top[ts] - 127);
       if constexpr (KIND != kPlain) {
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const uint4 b = lds.scales[ring][2 * ts + half][d];
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, floor2 = (top[ts] - 15u) * 0x00010001u;
+          const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, floor2 = (top[ts] - kBelow) * 0x00010001u;
           uint32_t s[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

@@ -41,8 +41,9 @@ extern "C" {
  *   k, v   [n_tok, Hkv, D] dtype dt, 16-byte aligned, token rows k_stride / v_stride
  *          elements apart (multiples of 8, at least Hkv * D)
  *   slots  [n_tok] page * page_size + offset (idx_page_tables); a negative slot or one
- *          past the last page is skipped. A call's slots are distinct, in any order; rows
- *          of consecutive slots share their stores.
+ *          past the last page is skipped. A call's slots are distinct (what a slot given
+ *          twice holds is unspecified), in any order; rows of consecutive slots share their
+ *          stores.
  * n_tok >= 0 (0: nothing is enqueued) and n_tok * ceil(Hkv / 2) below 2^28 (the launch;
  * larger calls are refused, IDX_ERR_INVALID_ARG), dt IDX_F32 or IDX_BF16.
  */
@@ -71,10 +72,11 @@ int idx_cache4_read(const int32_t* slots, const uint8_t* k_cache, const uint8_t*
  * of sizes and workspaces, with these differences:
  *   - a key meets its query as exact bf16 products with its scales in the key (no limit
  *     of their ratios): x is scale times their fp32 sum;
- *   - a probability is rounded to 11 bits (fp16), then takes its value's scale, exact
- *     while that is within 2^14 of the largest value scale among the row's 16 tokens from
- *     a multiple of 16 on (smaller ones count as zero), and meets the code, exact there;
- *     what reaches a row's sum is held to 2^-34 of its largest weight times value scale;
+ *   - a probability is rounded to 11 bits (fp16), then takes its value's scale, relative to
+ *     the largest that the row sees among its unit (16 tokens from a multiple of 16 on; one
+ *     2^25 or more below that counts as zero), and meets the code, exact there; a product of
+ *     weight and scale is off by up to 2^-33 of the row's largest product of a weight and its
+ *     unit's largest scale;
  *   - value scales are NaN or from 2^IDX_CACHE4_MIN_EXP to 2^IDX_CACHE4_MAX_EXP, as the
  *     write gives them (others: the outputs of the rows that see them are unspecified).
  * A NaN scale makes NaN of what it reaches: of a key, the rows that see the token; of a

@@ -318,6 +318,32 @@ def test_attend_long_rows_over_several_workgroups(B, n):
     attend_case(B, [n - 777 * b for b in range(B)], 4, 1, 16, rows=[0] if n > 50000 else None)
 
 
+def test_attend_uncut_rows_over_several_phases():
+    """More tiles than a workgroup lists at once, in rows that are not cut."""
+    c = Cache4(25, [20000], 1, 16)
+    R = 512
+    q, q64 = queries(c.rng, R, 2)
+    seen = np.full(R, 20000)
+    seen[1::2] = c.rng.integers(16000, 20001, R // 2)
+    assert idx.idx_attend4_workspace_bytes(R, 2, 1, c.max_pages) == 0
+    out = idx.idx_attend4(q.cuda(), *c.device(), i32(seen), c.max_pages, row_req=i32(np.zeros(R)))
+    check_rows(out, c, q64, np.zeros(R), seen, rows=[0, 1, 2, 3, 200, 511])
+
+
+def test_prefill_uncut_prompts_over_several_phases():
+    c = Cache4(26, [40000], 2, 16)
+    n, Hq = 2048, 64
+    q, q64 = queries(c.rng, n, Hq)
+    seen = np.arange(40000 - n, 40000) + 1
+    assert idx.idx_attend4_prefill_workspace_bytes(n, 1, Hq, 2, c.max_pages) == 0
+    c.vs[c.pages(0)[2100], 1, 3, 7] = 255           # in the second phase
+    out = idx.idx_attend4_prefill(q.cuda(), *c.device(), i32([0, n]), i32(seen), c.max_pages)
+    assert torch.isnan(out[:, 32:, 96:]).all() and torch.isfinite(out[:, :, :96]).all()
+    assert torch.isfinite(out[:, :32]).all()
+    keep = out[:, [0, 40]].clone()                  # two heads of the two groups
+    check_rows(keep, c, q64[:, [0, 40]], np.zeros(n), seen, rows=[0, 1, 777, n - 1])
+
+
 def test_attend_nan_scales_of_seen_tokens():
     """A key's NaN reaches the rows that see it; a value's its 32 dims of those rows, the
     others keep their bits."""
@@ -341,8 +367,8 @@ def test_attend_nan_scales_of_seen_tokens():
 
 
 def test_attend_value_scales_far_apart():
-    """Token by token: large values without weight cost the others no bits. Within a unit:
-    2^14 is kept."""
+    """Token by token: large values without weight cost the others no bits. Within a unit,
+    2^24 is kept."""
     c = Cache4(15, [900, 900], 1, 16)
     q, q64 = queries(c.rng, 2, 8)
     for b, grow in ((0, 1), (1, -1)):  # scales that grow, or fall, along the row
@@ -359,6 +385,23 @@ def test_attend_value_scales_far_apart():
     c.vs[p, 0, :, o] = 127 + 9
     out = idx.idx_attend4(q.cuda(), *c.device(), i32([300]), c.max_pages)
     check_rows(out, c, q.double().numpy(), [0], [300])
+
+
+def test_value_scales_far_apart_within_a_unit():
+    """Blocks of dims, and tokens, whose scales lie up to 2^24 apart among 16 tokens."""
+    for lens, news in (([900, 333], [1, 1]), ([900, 333], [9, 7]), ([900, 333], [200, 333])):
+        c = Cache4(22, lens, 2, 16)
+        c.vs[:] = 127 - c.rng.integers(0, 25, c.vs.shape)
+        c.vs[:, :, 2] = 127 - 20 - c.rng.integers(0, 5, c.vs[:, :, 2].shape)  # a small block
+        c.vs[:, :, 0, 0] = 127
+        c.poison_tails()
+        ptr, req = np.concatenate([[0], np.cumsum(news)]), np.repeat([0, 1], news)
+        seen = np.concatenate([np.arange(n - k, n) + 1 for n, k in zip(lens, news)])
+        q, q64 = queries(c.rng, len(req), 8)
+        out = idx.idx_attend4_prefill(q.cuda(), *c.device(), i32(ptr), i32(seen), c.max_pages)
+        check_rows(out, c, q64, req, seen, rows=range(0, len(req), 1 + len(req) // 40))
+        out = idx.idx_attend4(q.cuda(), *c.device(), i32(seen), c.max_pages, row_req=i32(req))
+        check_rows(out, c, q64, req, seen, rows=range(0, len(req), 1 + len(req) // 40))
 
 
 def test_attend_least_and_largest_scales():
