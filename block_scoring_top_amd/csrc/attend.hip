@@ -16,6 +16,7 @@ namespace {
 // scales.
 struct Cache8 {
   static constexpr bool kRowsInLds = false;
+  static constexpr bool kEven = false;
   template <int NT, int KIND, bool PACKED>
   static constexpr int kWaves = 2;
   struct Scratch {};

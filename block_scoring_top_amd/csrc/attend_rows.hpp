@@ -7,6 +7,7 @@
 //   kRowsInLds, rows   where add() finds the rows' operands: registers, or LDS, which all
 //                      waves share
 //   kWaves             waves a SIMD that an instance's registers are cut to
+//   kEven              whether chunks are lengthened until all workgroups run at once
 //
 // One token's query heads of one KV head are the 16 or 32 rows of the products (above 32
 // heads a group, two workgroups take 32 each); or, for prompt calls of few rows a request,
@@ -23,6 +24,7 @@ namespace idxk {
 
 constexpr int kAtNT = 256;
 constexpr int kAtWaves = kAtNT / kWave;
+constexpr int kAtCUs = 256;
 constexpr int kPhase = 256;                   // tiles whose pages wait in LDS
 constexpr int kPhaseUnits = 4 * kPhase;
 constexpr int kRowPad = kHeadDim + 4;         // floats of a row of sums in LDS
@@ -67,19 +69,11 @@ __global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) 
   };
   const PageList pages = known ? page_list(a, rt.b) : PageList{0, 0};
 
-  const float call_scale = fabsf(a.score_scale);
-  const Cap cap(a.softcap);
-  at_bf16x8 q[NT][4];
-  float slope2[NT];
   int len[NT];
   int seen = 0, shortest = 0x7FFFFFFF;  // longest and shortest visible length of the rows
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int64_t tok = token_of(16 * j + n);
-    const int hq = h * G + head_of(16 * j + n);
-    Cache::load_query(a.q + tok * a.q_stride + hq * kHeadDim, g, a.score_scale < 0.f, q[j]);
-    slope2[j] = KIND != kPlain ? slope_of(a, hq) : 0.f;
-    len[j] = known ? max(a.kv_len[tok], 0) : 0;
+    len[j] = known ? max(a.kv_len[token_of(16 * j + n)], 0) : 0;
     seen = max(seen, len[j]);
     shortest = min(shortest, len[j]);
   }
@@ -89,6 +83,65 @@ __global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) 
       seen = max(seen, __shfl_xor(seen, d));
       shortest = min(shortest, __shfl_xor(shortest, d));
     }
+  }
+  if constexpr (Cache::kEven && !PACKED) {
+    // A cut call's chunks: the host knows only a bound of the lengths and cuts for that. Where
+    // the lengths give more workgroups than the chip holds at once, the last of them would run
+    // by themselves: longer chunks, so that all run together (each row's last may be short).
+    // 4 rows of 4096 to 131072 tokens, 8 heads: 1064 workgroups of 1024 at once 69.7 us, 1008
+    // longer ones 67.2.
+    if (splits > 1 && a.ids == nullptr) {
+      __shared__ unsigned long long s_work[kAtWaves];
+      unsigned long long work = 0;
+      for (int i = tid; i < a.R; i += kAtNT) {
+        const int b = a.row_req == nullptr ? i : a.row_req[i];
+        if (b < 0 || b >= a.B) continue;
+        const int64_t held = (int64_t)page_list(a, b).n * upp;
+        const int64_t sees = ((int64_t)max(a.kv_len[i], 0) + kUnit - 1) / kUnit;
+        work += (min(held, sees) + 3) / 4;
+      }
+#pragma unroll
+      for (int d = 1; d < kWave; d *= 2) work += __shfl_xor(work, d);
+      if (lane == 0) s_work[w] = work;
+      __syncthreads();
+      work = 0;
+#pragma unroll
+      for (int i = 0; i < kAtWaves; ++i) work += s_work[i];
+      const int pairs = a.R * a.Hkv * bands;
+      const int room = kAtCUs * Cache::template kWaves<NT, KIND, PACKED> - pairs;
+      if (room >= pairs)
+        chunk = (int)min((unsigned long long)0x7FFFFFFF / 4,
+                         max((unsigned long long)chunk, (work * a.Hkv * bands + room - 1) / room));
+    }
+  }
+  const int64_t listed =
+      a.ids != nullptr ? (int64_t)a.K * upp
+                       : min((int64_t)pages.n * upp, ((int64_t)seen + kUnit - 1) / kUnit);
+  const int64_t end = min(listed, ((int64_t)split + 1) * chunk * 4);
+  auto part_of = [&](int row) {
+    return ((token_of(row) * a.Hkv + h) * splits + split) * G + head_of(row);
+  };
+  // Chunks behind a row's last token leave no sums, a weight of zero alone (the join takes no
+  // sums of those): calls are cut for a bound of the lengths, so there may be many (984 of 2048
+  // workgroups in the rows of 4096 to 131072 tokens: 71.4 us with zeros stored for them, 69.7).
+  if (splits > 1 && (int64_t)split * chunk * 4 >= end) {
+    for (int row = tid; row < rows; row += kAtNT) {
+      a.part_ml[2 * part_of(row)] = -__builtin_inff();
+      a.part_ml[2 * part_of(row) + 1] = 0.f;
+    }
+    return;
+  }
+
+  const float call_scale = fabsf(a.score_scale);
+  const Cap cap(a.softcap);
+  at_bf16x8 q[NT][4];
+  float slope2[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int hq = h * G + head_of(16 * j + n);
+    Cache::load_query(a.q + token_of(16 * j + n) * a.q_stride + hq * kHeadDim, g,
+                      a.score_scale < 0.f, q[j]);
+    slope2[j] = KIND != kPlain ? slope_of(a, hq) : 0.f;
   }
   if (Cache::kRowsInLds && w == 0) {  // (the waves meet at the first phase)
 #pragma unroll
@@ -102,10 +155,6 @@ __global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) 
 
   // this workgroup's units, list slots or selected slots of 16 tokens each, a phase at a
   // time
-  const int64_t listed =
-      a.ids != nullptr ? (int64_t)a.K * upp
-                       : min((int64_t)pages.n * upp, ((int64_t)seen + kUnit - 1) / kUnit);
-  const int64_t end = min(listed, ((int64_t)split + 1) * chunk * 4);
   for (int64_t u0 = (int64_t)split * chunk * 4; u0 < end; u0 += kPhaseUnits) {
     const int units = (int)min(end - u0, (int64_t)kPhaseUnits);
     const int tiles = (units + 3) / 4;
@@ -173,7 +222,7 @@ __global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) 
   for (int item = tid; item < rows * 16; item += kAtNT) {
     const int row = item >> 4, d = (item & 15) * 8, g_row = head_of(row);
     const int64_t tok = token_of(row);
-    const int64_t part = (((tok * a.Hkv + h) * splits) + split) * G + g_row;
+    const int64_t part = part_of(row);
     float m = s_m[0][row], l = 0.f;
 #pragma unroll
     for (int i = 1; i < kAtWaves; ++i) m = fmaxf(m, s_m[i][row]);
