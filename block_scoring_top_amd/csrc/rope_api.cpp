@@ -10,7 +10,7 @@
 namespace {
 
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
-constexpr int kMaxTokens = 1 << 26;  // 64 threads each: what a launch holds
+constexpr int kMaxTokens = 1 << 24;  // 256 threads each: what a launch holds
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 constexpr double kMaxFreq = 4;
 

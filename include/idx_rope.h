@@ -62,7 +62,7 @@ int idx_rope_table(double base, int rot, int kind, double stretch, double origin
  * Angles come from the table's whole numbers without rounding, sine, cosine and sums are
  * fp32: off by at most 2^-21 * |factor| * (|a| + |b|), then rounded once to dt.
  * rot a multiple of 16, 16 <= rot <= D; first a multiple of 8, first + rot <= D; factor
- * finite; n_tok >= 0 (0: nothing is enqueued) and below 2^26 (the launch), Hq >= 1, Hkv >= 0;
+ * finite; n_tok >= 0 (0: nothing is enqueued) and below 2^24 (the launch), Hq >= 1, Hkv >= 0;
  * dt IDX_F32 or IDX_BF16.
  */
 int idx_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,

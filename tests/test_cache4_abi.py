@@ -110,7 +110,7 @@ ROPE = dict(q=P, k=P, q_stride=2048, k_stride=512, tok_len=P, turns=P, q_out=P, 
     (dict(q_stride=2040), INVALID), (dict(q_out_stride=2052), INVALID),
     (dict(k_stride=504), INVALID), (dict(k_out_stride=516), INVALID),
     (dict(q_out_stride=4096), INVALID),  # in place, other rows
-    (dict(k_out_stride=1024), INVALID), (dict(n_tok=-1), INVALID), (dict(n_tok=1 << 26), INVALID),
+    (dict(k_out_stride=1024), INVALID), (dict(n_tok=-1), INVALID), (dict(n_tok=1 << 24), INVALID),
     (dict(Hq=0), INVALID), (dict(Hkv=-1), INVALID), (dict(first=-8), INVALID),
     (dict(first=8), INVALID), (dict(rot=0), INVALID), (dict(rot=17), INVALID),
     (dict(rot=130), INVALID), (dict(factor=math.nan), INVALID), (dict(factor=math.inf), INVALID),

@@ -81,7 +81,6 @@ def test_rope_parts_and_layouts(rot, first, adjacent, dtype):
 
 @pytest.mark.parametrize("n", [1, 2, 3, 2047, 2048, 2049, 4099, 5002])
 def test_rope_many_tokens(n):
-    """On both sides of the rule that gives a workgroup several tokens."""
     rng = np.random.default_rng(n)
     q, k = rows(rng, n, 3, torch.bfloat16), rows(rng, n, 1, torch.bfloat16)
     tok_len = rng.integers(-3, 200000, n)
