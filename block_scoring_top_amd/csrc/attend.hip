@@ -166,8 +166,9 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
 // batch of 128 rows on 4 heads, 256 pages each: 102 us whole, 108 in two). Then into
 // chunks that would give eight a CU if all rows were of the longest length, so that
 // ragged rows still balance (4 rows of 4096 to 131072 tokens on 8 heads: 148 us at two a
-// CU, 136 at four, 123 at eight, 127 at sixteen; equal shares for all that the chip holds at
-// once, worked out by the kernel, are slower, 130), down to a tile for each wave.
+// CU, 136 at four, 123 at eight, 127 at sixteen; 114 at eight today; equal shares for all that
+// the chip holds at once, worked out by the kernel, were slower, 130), down to a tile for each
+// wave.
 AttnSplit attend_rows_split(int64_t R, int Hkv, int64_t units) {
   const int64_t tiles = (units + 3) / 4;
   const int64_t pairs = R * Hkv;

@@ -114,7 +114,9 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
   const float call_scale = fabsf(a.score_scale);
   const Cap cap(a.softcap);
 
-  int longest = len, shortest = row < rows ? len : 0x7FFFFFFF;  // of the wave's rows
+  // of the wave's rows (one that sees nothing keeps no tile from being seen whole: its
+  // probabilities are zeros, and its sums are not taken)
+  int longest = len, shortest = len > 0 ? len : 0x7FFFFFFF;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     longest = max(longest, __shfl_xor(longest, d));
@@ -443,15 +445,17 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
   if (row >= rows) return;
   // lane: dims 32 dt + 8 q + 4 half + e of its row
   if (splits == 1) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
     uint16_t* out = a.out + (tok * a.Hq + hq) * kHeadDim;
 #pragma unroll
     for (int dt = 0; dt < 4; ++dt)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<uint2*>(out + 32 * dt + 8 * g + 4 * half) =
-            make_uint2(pack_bf16(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv),
-                       pack_bf16(o[dt][4 * g + 2] * inv, o[dt][4 * g + 3] * inv));
+      for (int g = 0; g < 4; ++g) {
+        const uint2 y = make_uint2(pack_bf16(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv),
+                                   pack_bf16(o[dt][4 * g + 2] * inv, o[dt][4 * g + 3] * inv));
+        *reinterpret_cast<uint2*>(out + 32 * dt + 8 * g + 4 * half) = none ? make_uint2(0, 0) : y;
+      }
   } else {
     const int64_t part = (((tok * a.Hkv + h) * splits) + split) * G + hq % G;
     float* out = a.part_o + part * kHeadDim;

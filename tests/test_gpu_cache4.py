@@ -1,5 +1,7 @@
 """The paged 4-bit cache on the GPU against its CPU oracle: writes and reads exactly,
 attention within bounds derived from its arithmetic (tests/cache4_helpers.py)."""
+import os
+import re
 import sys
 
 import numpy as np
@@ -178,6 +180,24 @@ def test_read_any_order_repeats_and_unknown_slots():
                 big = np.abs(want) > 2.0 ** 126  # poisoned pages' scales: 2^127 and NaN
                 np.testing.assert_array_equal(got[~big], want[~big])
         assert (y[:, :, 3] == 3.0).all()
+
+
+def test_read_one_side():
+    """Keys alone, or values alone: the other pointer is NULL."""
+    c = Cache4(28, [100], 2, 16)
+    slots = i32(np.concatenate([np.arange(100) % 60, [-1]]))
+    kc, vc, ks, vs = state(c)
+    k, v = idx.idx_cache4_read(slots, kc, vc, ks, vs, dtype=torch.float32)
+    lib = idx.load()
+    for side, want in ((0, k), (1, v)):
+        out = torch.full_like(want, 5.0)
+        ptr = [None, None]
+        ptr[side] = out.data_ptr()
+        assert lib.idx_cache4_read(slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+                                   vs.data_ptr(), *ptr, 256, 256, slots.numel(), 2, 128,
+                                   c.n_pages, 16, 0, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
 
 
 def test_calls_past_4gib():
@@ -480,6 +500,21 @@ def test_prefill_any_lengths_and_empty_rows():
         seen = np.concatenate([rng.integers(-2, n + 1, k) for n, k in zip(lens, news)])
         seen[:3] = [0, -5, 64]
         prefill_case(8, lens, news, 8, 2, 16, seen=seen)
+
+
+@pytest.mark.parametrize("lens,news", [([300], [300]), ([6000], [130])])
+def test_prefill_empty_rows_beside_nan_scales(lens, news):
+    """Rows that see nothing are zero whatever the tiles of the others hold, cut or not."""
+    c = Cache4(27, lens, 2, 16)
+    n = news[0]
+    seen = np.arange(lens[0] - n, lens[0]) + 1
+    seen[::7], seen[3] = 0, -4
+    c.vs[c.pages(0)[0], 1, 2, 3] = 255
+    q, q64 = queries(c.rng, n, 8)
+    out = idx.idx_attend4_prefill(q.cuda(), *c.device(), i32([0, n]), i32(seen), c.max_pages)
+    check_rows(out, c, q64, np.zeros(n), seen, rows=range(0, n, 3))
+    assert not out[::7].any() and not out[3].any()
+    assert torch.isnan(out[torch.from_numpy(seen > 3).cuda()][:, 4:, 64:96]).all()
 
 
 def test_prefill_leaves_other_rows_as_they_were():
@@ -801,3 +836,43 @@ def test_typed_caches_and_binding_checks():
                 lambda: idx.idx_cache4_write(x.half(), x.half(), n, kc, vc, ks, vs)):
         with pytest.raises(TypeError):
             bad()
+
+
+def test_readme_lines_run():
+    """The lines that README.md shows, as they stand, after a step of page tables."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                           "README.md")) as f:
+        blocks = [b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S)
+                  if "idx_cache4_write" in b]
+    assert len(blocks) == 1
+    B, Hq, Hkv, page, max_pages = 3, 8, 2, 16, 4
+    n_pages = 2 * B * max_pages
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
+    t = idx.idx_page_tables(i32([0] * B), i32([20, 7, 33]), table, i32(np.arange(n_pages)),
+                            i32([0, n_pages]), 60, page_size=page)
+    rows = torch.randn(60, Hq + 2 * Hkv, 128, device="cuda").bfloat16()
+    kept = t.slots[:60] >= 0
+    scope = dict(
+        idx=idx, torch=torch, t=t, max_pages=max_pages, q=rows[:, :Hq], k=rows[:, Hq:Hq + Hkv],
+        v=rows[:, Hq + Hkv:], gq=torch.randn(60, Hq, 128, device="cuda"),
+        gk=torch.randn(60, Hkv, 128, device="cuda"),
+        k_cache=torch.zeros(n_pages, Hkv, page, 64, **u8),
+        v_cache=torch.zeros(n_pages, Hkv, 128, page // 2, **u8),
+        k_scale=torch.zeros(n_pages, Hkv, page, 4, **u8),
+        v_scale=torch.zeros(n_pages, Hkv, 4, page, **u8),
+        slots=t.slots, shift_plus_1=i32(np.full(60, 6)),
+        new_slots=torch.where(kept, t.slots + B * max_pages * page, -1))
+    turned = idx.idx_rope(rows[:, :Hq].contiguous(), None, t.tok_len,
+                          idx.idx_rope_table(128, base=5e5, kind="by_turns", stretch=8.0,
+                                             original=8192.0, lo=1.0, hi=4.0))[0]
+    exec(blocks[0], scope)
+    assert torch.equal(rows[:, :Hq], torch.where(kept[:, None, None], turned, rows[:, :Hq]))
+    back = idx.idx_cache4_read(scope["new_slots"], *scope["cache4"], dtype=torch.float32)
+    first = idx.idx_cache4_read(t.slots, *scope["cache4"], dtype=torch.float32)
+    assert torch.equal(back[1], first[1]) and not torch.equal(back[0], first[0])
+    one = idx.idx_attend4(scope["q"], *scope["cache4"], t.kv_indptr, t.kv_indices, t.tok_len,
+                          max_pages, row_req=t.tok_req)
+    # (each side is within 2^-8 of its value, and what its sums add is far below 2^-8)
+    off = (one[kept].float() - scope["out"][kept].float()).abs()
+    assert float((off / (one[kept].float().abs() + 1)).max()) < 2.0 ** -6
