@@ -151,7 +151,6 @@ struct Cache4 {
   // where nothing spills for it (4 rows of 4096 to 131072 tokens 73.7 us with three, 71.0 with
   // four; 128 rows of 256 selected pages, two workgroups a CU, 57.5 and 57.2).
   static constexpr bool kRowsInLds = true;
-  static constexpr bool kEven = true;
   template <int NT, int KIND, bool PACKED>
   static constexpr int kWaves = NT == 1 && !PACKED && KIND == kPlain ? 4 : NT == 1 ? 3 : 2;
   // A unit's value scales, and those as fp16 factors: written by the 16 lanes of its group, a

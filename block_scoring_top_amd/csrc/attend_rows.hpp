@@ -7,7 +7,6 @@
 //   kRowsInLds, rows   where add() finds the rows' operands: registers, or LDS, which all
 //                      waves share
 //   kWaves             waves a SIMD that an instance's registers are cut to
-//   kEven              whether chunks are lengthened until all workgroups run at once
 //
 // One token's query heads of one KV head are the 16 or 32 rows of the products (above 32
 // heads a group, two workgroups take 32 each); or, for prompt calls of few rows a request,
@@ -24,7 +23,6 @@ namespace idxk {
 
 constexpr int kAtNT = 256;
 constexpr int kAtWaves = kAtNT / kWave;
-constexpr int kAtCUs = 256;
 constexpr int kPhase = 256;                   // tiles whose pages wait in LDS
 constexpr int kPhaseUnits = 4 * kPhase;
 constexpr int kRowPad = kHeadDim + 4;         // floats of a row of sums in LDS
@@ -82,36 +80,6 @@ __global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) 
     for (int d = 1; d < 16; d *= 2) {
       seen = max(seen, __shfl_xor(seen, d));
       shortest = min(shortest, __shfl_xor(shortest, d));
-    }
-  }
-  if constexpr (Cache::kEven && !PACKED) {
-    // A cut call's chunks: the host knows only a bound of the lengths and cuts for that. Where
-    // the lengths give more workgroups than the chip holds at once, the last of them would run
-    // by themselves: longer chunks, so that all run together (each row's last may be short).
-    // 4 rows of 4096 to 131072 tokens, 8 heads: 1064 workgroups of 1024 at once 69.7 us, 1008
-    // longer ones 67.2.
-    if (splits > 1 && a.ids == nullptr) {
-      __shared__ unsigned long long s_work[kAtWaves];
-      unsigned long long work = 0;
-      for (int i = tid; i < a.R; i += kAtNT) {
-        const int b = a.row_req == nullptr ? i : a.row_req[i];
-        if (b < 0 || b >= a.B) continue;
-        const int64_t held = (int64_t)page_list(a, b).n * upp;
-        const int64_t sees = ((int64_t)max(a.kv_len[i], 0) + kUnit - 1) / kUnit;
-        work += (min(held, sees) + 3) / 4;
-      }
-#pragma unroll
-      for (int d = 1; d < kWave; d *= 2) work += __shfl_xor(work, d);
-      if (lane == 0) s_work[w] = work;
-      __syncthreads();
-      work = 0;
-#pragma unroll
-      for (int i = 0; i < kAtWaves; ++i) work += s_work[i];
-      const int pairs = a.R * a.Hkv * bands;
-      const int room = kAtCUs * Cache::template kWaves<NT, KIND, PACKED> - pairs;
-      if (room >= pairs)
-        chunk = (int)min((unsigned long long)0x7FFFFFFF / 4,
-                         max((unsigned long long)chunk, (work * a.Hkv * bands + room - 1) / room));
     }
   }
   const int64_t listed =
