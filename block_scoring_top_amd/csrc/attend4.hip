@@ -15,8 +15,21 @@
 
 namespace idxk {
 
-AttnSplit attend4_rows_split(int64_t R, int Hkv, int64_t units) {
-  return attend_rows_split(R, Hkv, units);
+// Rows are cut as the 8-bit cache's (attend.hip), into chunks that would give eight
+// workgroups a CU if all rows were of the longest length, so that ragged ones balance; but for
+// two a CU, all that it holds, where a chunk is more than its start and its part of the join:
+// groups above 16 heads, whose instance has two workgroups a CU and twice the partial sums
+// (16 rows of 8192 to 32768 tokens, 64 heads on 2: 51 us with eight, 40 with two; 4 of 4096 to
+// 131072: 45 and 37), and a row by itself (131072 tokens, 32 heads on 8: 42 and 35). Ragged rows
+// of smaller groups: 4 of 4096 to 131072, 32 heads on 8, 70 with eight, 82 with two.
+AttnSplit attend4_rows_split(int64_t R, int Hkv, int G, int64_t units) {
+  const int64_t tiles = (units + 3) / 4, pairs = R * Hkv;
+  const int64_t want = G > 16 || R == 1 ? 512 : 2048;
+  int64_t splits = pairs >= 512 ? 1 : (want + pairs - 1) / pairs;
+  if (splits > tiles / kAtWaves) splits = tiles / kAtWaves;
+  if (splits < 1) splits = 1;
+  const int64_t chunk = (tiles + splits - 1) / splits;
+  return {(int)chunk, (int)((tiles + chunk - 1) / chunk), 0};
 }
 
 int launch_attend4_rows(const AttnArgs& a, AttnSplit sp, void* stream) {

@@ -129,9 +129,9 @@ int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
 }
 
 // How the rows of a call are cut.
-idxk::AttnSplit single_split(int bits, int R, int Hkv, int64_t units) {
+idxk::AttnSplit single_split(int bits, int R, int Hq, int Hkv, int64_t units) {
   return bits == 8 ? idxk::attend_rows_split(R, Hkv, units)
-                   : idxk::attend4_rows_split(R, Hkv, units);
+                   : idxk::attend4_rows_split(R, Hkv, Hq / Hkv, units);
 }
 idxk::AttnSplit packed_split(int bits, int n_tok, int B, int Hq, int Hkv, int64_t units) {
   return bits == 8 ? idxk::attend_prefill_split(n_tok, B, Hq, Hkv, units)
@@ -141,7 +141,7 @@ idxk::AttnSplit packed_split(int bits, int n_tok, int B, int Hq, int Hkv, int64_
 size_t single_bytes(int bits, int R, int Hq, int Hkv, int max_pages, int K, int page_size) {
   if (R < 1 || K < 0 || !shape_ok(R, 1, Hq, Hkv, max_pages, page_size)) return 0;
   return partial_bytes(
-      R, Hq, single_split(bits, R, Hkv, row_units(max_pages, K, page_size)).splits);
+      R, Hq, single_split(bits, R, Hq, Hkv, row_units(max_pages, K, page_size)).splits);
 }
 
 // idx_attend over the cache of so many bits, and idx_attend_prefill
@@ -161,7 +161,7 @@ int attend_single(int bits, const void* q, int64_t q_stride, const uint8_t* k_ca
     return IDX_ERR_INVALID_ARG;
   if ((int64_t)K * page_size > kMaxInt) return IDX_ERR_INVALID_ARG;
   if (R == 0) return IDX_OK;
-  const idxk::AttnSplit sp = single_split(bits, R, Hkv, row_units(max_pages, K, page_size));
+  const idxk::AttnSplit sp = single_split(bits, R, Hq, Hkv, row_units(max_pages, K, page_size));
   // 256 threads for each of at most two workgroups a row, KV head and split (rows are cut,
   // and joined, only where rows times KV heads are a few hundred)
   if ((int64_t)R * Hkv * sp.splits * (Hq / Hkv > 32 ? 2 : 1) * 256 > kMaxThreads)

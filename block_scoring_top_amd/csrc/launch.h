@@ -94,7 +94,7 @@ int64_t attend_prefill_tiles(int64_t n_tok, int B, int G, int per);  // of `per`
 int launch_attend_rows(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
 // the 4-bit cache (idx_attend4, idx_attend4_prefill)
-AttnSplit attend4_rows_split(int64_t R, int Hkv, int64_t units);
+AttnSplit attend4_rows_split(int64_t R, int Hkv, int G, int64_t units);
 AttnSplit attend4_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units);
 int launch_attend4_rows(const AttnArgs& a, AttnSplit sp, void* stream);
 int launch_attend4_prefill(const AttnArgs& a, AttnSplit sp, void* stream);
