@@ -2,7 +2,7 @@
 // idx_attend4): the rows' kernel of attend_rows.hpp over the tile of attend4.hpp. Bound by
 // reading the cache, 136 bytes a token and KV head: 128 rows of 256 selected pages, 4 heads,
 // 286 MB in 57 us, 5.0 TB/s (a plain read reaches 5.8 on this card; the same loads without
-// the arithmetic take 53.5); 4 rows of 4096 to 131072 tokens, 8 heads, 294 MB in 64 us and 5
+// the arithmetic take 53.5); 4 rows of 4096 to 131072 tokens, 8 heads, 294 MB in 65 us and 5
 // of joining. What led there: 64 and 85 us with each lane making all factors of its unit's
 // value scales and masks taken in every tile; 57 and 75 with the factors made once and masks
 // behind branches; then occupancy and the cut (attend_rows.hpp). The next tile's loads held in

@@ -16,7 +16,7 @@
 // the 16 tokens of two dims, 16 bytes, and a unit's 1 KB is written (read) in one go where
 // the page is the unit. 16396 tokens of 8 heads (bf16, 88 MB in and out): written in 13.5 us,
 // read back in 12 (inputs partly in the last-level cache); 63280 read in 62, 5.3 TB/s (a
-// large copy runs at 4.9); 128 single tokens of 4 heads 4.8 and 3.3 us.
+// large copy runs at 4.9); 128 single tokens of 4 heads 4.3 and 3.2 us.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"

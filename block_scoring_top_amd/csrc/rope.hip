@@ -10,7 +10,7 @@
 // lanes take a head's row, 16 elements each: 8 pairs, or 16 elements that pass unchanged (four
 // tokens a workgroup: 16384 tokens 69.8 us, 64.6 so). 16200 tokens of 32 + 8
 // heads in bf16, 332 MB in and out: 61 us, 5.5 TB/s (a large copy runs at 4.9); 4100 tokens
-// of 16 + 2 in fp32 17 us, 4.4 TB/s; 128 tokens of 16 + 4 3.3 us, a launch and two loads
+// of 16 + 2 in fp32 17 us, 4.4 TB/s; 128 tokens of 16 + 4 3.2 us, a launch and two loads
 // behind each other.
 #include <hip/hip_runtime.h>
 
