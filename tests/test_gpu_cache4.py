@@ -876,3 +876,25 @@ def test_readme_lines_run():
     # (each side is within 2^-8 of its value, and what its sums add is far below 2^-8)
     off = (one[kept].float() - scope["out"][kept].float()).abs()
     assert float((off / (one[kept].float().abs() + 1)).max()) < 2.0 ** -6
+
+
+def test_workspaces_may_hold_anything():
+    """Chunks behind a row's end leave no sums: what the workspace held there does not reach
+    the output, in either join (few items, many)."""
+    for B, Hq in ((3, 8), (40, 64)):
+        lens = [(500 + 997 * b) % 9000 for b in range(B)]
+        c = Cache4(50, lens, 2, 16)
+        q, _ = queries(c.rng, B, Hq)
+        args = (q.cuda(), *c.device())
+        bound = 3 * c.max_pages
+        ptr, n = i32(np.arange(B + 1)), i32(lens)
+        for call, size, rest in (
+                (idx.idx_attend4, idx.idx_attend4_workspace_bytes(B, Hq, 2, bound), (n,)),
+                (idx.idx_attend4_prefill,
+                 idx.idx_attend4_prefill_workspace_bytes(B, B, Hq, 2, bound), (ptr, n))):
+            assert size > 0
+            outs = [call(*args, *rest, bound,
+                         ws=torch.full((size,), fill, dtype=torch.uint8, device="cuda"))
+                    for fill in (0, 255, 127)]
+            assert torch.isfinite(outs[0]).all()
+            assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
