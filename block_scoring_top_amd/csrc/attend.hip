@@ -73,7 +73,11 @@ struct Cache8 {
 // teams of 32 lanes, four dims a lane, take every TEAMS-th split, four at a time, and are
 // joined in LDS. Fixed orders: the same sums every time. Short: a launch and chains of loads
 // (64 splits of 128 items: 4.9 us with eight splits' loads in flight, 5.7 with the sums behind
-// the weights of four).
+// the weights of four). A split's weights may reach 2^60 in its maximum's units (attend4.hpp), and
+// count where its sums do not: scaled_down takes them where a factor of 2^-126 would leave
+// more than 2^-29 of a row's weights, 2^-57 at the least (1024 items of 64 splits: 0.9 us if it
+// always did).
+constexpr float kHeavy = 0x1p40f;
 template <int TEAMS>
 __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t items,
                                                              int splits) {
@@ -124,15 +128,26 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
         for (int i = j; i < j + kStep; ++i) top = fmaxf(top, ml[i][0]);
         const float base = top == -__builtin_inff() ? 0.f : top;
         const float f = exp2_fast(m - base);
+        float most = l;
+#pragma unroll
+        for (int i = j; i < j + kStep; ++i) most = fmaxf(most, ml[i][1]);
+        float w[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) w[i] = exp2_fast(ml[j + i][0] - base);
+        if (__any(most > kHeavy)) {
+          l = scaled_down(l, m - base);
+#pragma unroll
+          for (int i = 0; i < kStep; ++i)
+            l += scaled_down(ml[j + i][1], ml[j + i][0] - base);
+        } else {
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < kStep; ++i) l += ml[j + i][1] * w[i];
+        }
         m = top;
-        l *= f;
         o *= f;
 #pragma unroll
-        for (int i = j; i < j + kStep; ++i) {
-          const float w = exp2_fast(ml[i][0] - base);
-          l += ml[i][1] * w;
-          o += x[i] * w;
-        }
+        for (int i = 0; i < kStep; ++i) o += x[j + i] * w[i];
       }
     }
   }
@@ -148,12 +163,12 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
   for (int i = 1; i < TEAMS; ++i) top = fmaxf(top, s_m[group + i]);
   const float base = top == -__builtin_inff() ? 0.f : top;
   const float f = exp2_fast(m - base);
-  l *= f;
+  l = scaled_down(l, m - base);
   o *= f;
 #pragma unroll
   for (int i = 1; i < TEAMS; ++i) {
     const float w = exp2_fast(s_m[group + i] - base);
-    l += s_l[group + i] * w;
+    l += scaled_down(s_l[group + i], s_m[group + i] - base);
     o += *reinterpret_cast<const at_f32x4*>(&s_o[group + i][4 * lane]) * w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;

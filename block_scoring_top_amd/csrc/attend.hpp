@@ -72,6 +72,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// x 2^d, d <= 0, also where 2^d alone would be flushed to zero (below 2^-126) and x 2^d is not.
+// (From d = -120 up the first factor is 1: the product is x times the second's, as it stands.)
+__device__ __forceinline__ float scaled_down(float x, float d) {
+  return x * exp2_fast(fminf(d + 120.f, 0.f)) * exp2_fast(fmaxf(d, -120.f));
+}
 
 // over the four lane groups of one query row
 __device__ __forceinline__ float groups_max(float v) {

@@ -16,7 +16,10 @@
 // The reference of a row's sums is the running maximum of score + log2(the unit's largest
 // value scale): what it bounds is the products of weight and value, not the weights, so
 // that one token with large values and no weight costs the others no bits. Both the sums
-// and the sum of weights are held in units of it (weights reach 2^60 then, in fp32).
+// and the sum of weights are held in units of it. Weights reach 2^60 then, in fp32, and the
+// reference moves by up to 2^120 more than the scores do, which no single exponential holds: the
+// sum of weights moves in two (scaled_down), and the exponentials of a unit far below the
+// reference take along more than its scale (far_scale).
 #pragma once
 
 #include "attend.hpp"
@@ -26,6 +29,21 @@ namespace idxk {
 typedef uint16_t at_u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kNanScale = 255;
+
+// The exponent that a unit's exponentials take along, and the sum of weights gives back: its
+// largest scale's, lv, or, where its best product of weight and scale, 2^best, lies 2^kFar or
+// more below the reference, as much more as brings it there. The probabilities of such a unit
+// are zeros in fp16 either way; its weights may count all the same, with scales up to 2^120
+// apart, and keep the bits of those down to 2^-35 of the unit's largest (exponentials below
+// 2^-126 are zeros). At most the largest scale's 60: what is below the reference then still has a
+// weight of 2^-100 of the row's largest or less.
+// (The largest scales, 2^60, lie 2^kFar above those of kLowTop: units from there on need none of
+// this.)
+constexpr float kFar = 100.f;
+constexpr uint32_t kLowTop = 127 - 40;
+__device__ __forceinline__ float far_scale(float lv, float best, float m) {
+  return fminf(fmaxf(lv, floorf(m - kFar - (best - lv))), 60.f);
+}
 
 // eight codes times the scale -> bf16, exact
 __device__ __forceinline__ at_bf16x8 codes4_bf16(uint32_t w, float scale) {
@@ -262,19 +280,26 @@ struct Cache4 {
           for (int t = 0; t < 16; ++t)
             if (t >= min(have, len[j] - pos)) x[j][t >> 2][t & 3] = -__builtin_inff();
         }
-        float best = -__builtin_inff();
+        float unit = -__builtin_inff();  // this lane's unit's best product
 #pragma unroll
-        for (int t = 0; t < 16; ++t) best = fmaxf(best, x[j][t >> 2][t & 3]);
-        best = groups_max(__builtin_fmaf(best, sc, lv));
+        for (int t = 0; t < 16; ++t) unit = fmaxf(unit, x[j][t >> 2][t & 3]);
+        unit = __builtin_fmaf(unit, sc, lv);
+        const float best = groups_max(unit);
         if (__any(best > st.m[j] + kLazy)) {
           const float m = best > st.m[j] + kLazy ? best : st.m[j];
-          const float f = exp2_fast(st.m[j] - (m == -__builtin_inff() ? 0.f : m));
+          const float d = st.m[j] - (m == -__builtin_inff() ? 0.f : m), f = exp2_fast(d);
           st.m[j] = m;
-          st.l[j] *= f;
+          st.l[j] = scaled_down(st.l[j], d);
 #pragma unroll
           for (int dt = 0; dt < 8; ++dt) st.o[j][dt] *= f;
         }
-        const float off = (st.m[j] == -__builtin_inff() ? 0.f : st.m[j]) - kPBias - lv;
+        float take = lv, back = unlv;
+        if (__any(unit < st.m[j] - kFar)) {
+          asm volatile("");  // a branch: few tiles are that far
+          take = far_scale(lv, unit, st.m[j]);
+          back = exp2_fast(-take);
+        }
+        const float off = (st.m[j] == -__builtin_inff() ? 0.f : st.m[j]) - kPBias - take;
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -287,7 +312,7 @@ struct Cache4 {
           p[j][2 * s] = pack_f16(e[0], e[1]);
           p[j][2 * s + 1] = pack_f16(e[2], e[3]);
         }
-        st.l[j] = __builtin_fmaf(sum[0] + sum[1], unlv, st.l[j]);
+        st.l[j] = __builtin_fmaf(sum[0] + sum[1], back, st.l[j]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kAtNT, (Cache::template kWaves<NT, KIND, PACKED>)) 
     for (int i = 1; i < kAtWaves; ++i) m = fmaxf(m, s_m[i][row]);
     const float base = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
-    for (int i = 0; i < kAtWaves; ++i) l += s_l[i][row] * exp2_fast(s_m[i][row] - base);
+    for (int i = 0; i < kAtWaves; ++i) l += scaled_down(s_l[i][row], s_m[i][row] - base);
     const float* o = &s_o[row][d];
     if (splits == 1) {
       const float inv = l == 0.f ? 0.f : 1.f / l;

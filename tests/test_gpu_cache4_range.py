@@ -1,0 +1,115 @@
+"""Attention over the 4-bit cache at the ends of the value scales' range, against the float64
+oracle. The bound is the one of tests/cache4_helpers.py with the largest product of a weight
+and its unit's largest scale where that one has their sum:
+  - a weight is rounded to fp16, 2^-11 of itself or 2^-25 where it is small, and its product
+    with a scale by 2^-25 again, in units where the row's largest such product is 2^9 or more;
+    a code is at most 6: 6 * 2^-33 of the largest product for each token;
+  - the sum of weights loses no more than 2^-35 of the largest weight for each token, far
+    below its 2^-24 a token of rounding.
+"""
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import paged_cache as pc
+from tests.cache4_helpers import Cache4
+from tests.cache_helpers import U
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import block_scoring_top_amd as idx  # noqa: E402
+
+
+def i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+def expected(c, q, b, seen, scale, h=0):
+    """One row and query head q [128]: its output and how far off it may be."""
+    k, v, there, top = c.tokens(b, h)
+    out, absum, mag = pc.attend(q, k, v, there, seen, None, c.page, scale)
+    n = min(seen, len(k))
+    x = k[:n] @ q * scale
+    w = np.exp(x - x.max())
+    w /= w.sum()
+    unit = np.pad(top[:n], (0, -n % 16)).reshape(-1, 16).max(1).repeat(16)[:n]
+    weights = 2 * np.expm1(160 * U * mag + 4 * U) + 2.0 ** -11 + (2 * n + 8) * U
+    off = absum * weights + n * 6 * 2.0 ** -33 * float((w * unit).max())
+    return out, off + (np.abs(out) + off) * 2.0 ** -8 + 2.0 ** -130
+
+
+def check(name, out, c, q, seen, scale):
+    """out [rows, Hq, 128], all rows and heads of request 0 with the query q [128] and the
+    visible length seen."""
+    want, tol = expected(c, q.double().numpy(), 0, seen, float(np.float32(scale)))
+    err = (out.double().cpu().numpy() - want) / tol
+    print(f"[range4] {name}: {np.abs(err).max():.2f} of the bound", flush=True)
+    sys.stdout.flush()
+    bad = np.argwhere(~(np.abs(err) <= 1))
+    assert bad.size == 0, (name, bad[0], float(out[tuple(bad[0])]), want[bad[0][-1]], tol[bad[0][-1]])
+
+
+def forms(c, q, n, scale):
+    """The outputs of each kernel and cut for rows that see the first n tokens: single rows,
+    cut and whole, few packed rows, and prompts whose rows see all tiles whole, or, with a
+    shorter row in each workgroup, in part."""
+    args, bound = c.device(), c.max_pages
+    rows = lambda r, h: q.bfloat16().cuda().expand(r, h, 128).contiguous()  # noqa: E731
+    kw = dict(scale=scale)
+    for r, h in ((1, 4), (1, 20), (512, 1)):
+        cut = idx.idx_attend4_workspace_bytes(r, h, 1, bound) > 0
+        out = idx.idx_attend4(rows(r, h), *args, i32([n] * r), bound, row_req=i32([0] * r), **kw)
+        yield f"{r} rows of {h} heads{', cut' if cut else ''}", out
+    for t, h in ((3, 4), (130, 2), (512, 64)):
+        cut = idx.idx_attend4_prefill_workspace_bytes(t, 1, h, 1, bound) > 0
+        seen = np.full(t, n)
+        name = f"{t} tokens of {h} heads{', cut' if cut else ''}"
+        out = idx.idx_attend4_prefill(rows(t, h), *args, i32([0, t]), i32(seen), bound, **kw)
+        yield name, out
+        seen[1::4] = 1
+        out = idx.idx_attend4_prefill(rows(t, h), *args, i32([0, t]), i32(seen), bound, **kw)
+        yield name + " among short ones", out[torch.from_numpy(seen == n).cuda()]
+
+
+def plain_cache(n):
+    """Keys of zeros, values of ones."""
+    c = Cache4(1, [n], 1, 16)
+    c.k[:], c.ks[:] = 0, 127
+    c.v[:], c.vs[:] = 2, 127
+    return c
+
+
+def put(c, t, name, codes, scale):
+    """Token t of request 0: codes [128] and scale bytes [4]."""
+    page, o = c.pages(0)[t // 16], t % 16
+    if name == "k":
+        c.k[page, 0, o], c.ks[page, 0, o] = codes, scale
+    else:
+        c.v[page, 0, :, o], c.vs[page, 0, :, o] = codes, scale
+
+
+@pytest.mark.parametrize("gap", [7.0, 12.0, 16.5, 40.0])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("n", [200, 1100, 9000])
+def test_many_least_scales_beside_one_largest(n, at, gap):
+    """Tokens of the least value scale, and one of the largest whose weight is 2^gap times
+    theirs: the largest product of weight and scale moves by 2^(120 + gap), the weights' sum
+    does not lose what it held, whichever comes first."""
+    c = plain_cache(n)
+    c.vs[:] = 67
+    key = np.zeros(128, np.uint8)
+    key[0] = 2
+    t = {"first": 0, "middle": n // 2, "last": n - 1}[at]
+    put(c, t, "k", key, 127)
+    put(c, t, "v", 2, 187)
+    c.poison_tails()
+    q = torch.zeros(128)
+    q[0] = gap
+    for name, out in forms(c, q, n, np.log(2)):
+        check(f"{n} tokens, {at}, 2^{gap}: {name}", out, c, q, n, np.log(2))
