@@ -54,14 +54,14 @@ __device__ __forceinline__ at_bf16x8 codes4_bf16(uint32_t w, float scale) {
                             two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
                             two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))));
 }
-// eight codes -> fp16, exact
-__device__ __forceinline__ at_f16x8 codes4_f16(uint32_t w) {
+// eight codes times 1 or 2 -> fp16, exact
+__device__ __forceinline__ at_f16x8 codes4_f16(uint32_t w, float scale = 1.f) {
   auto two = [](auto r) { return __builtin_bit_cast(uint32_t, r); };
   return __builtin_bit_cast(
-      at_f16x8, make_uint4(two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 0)),
-                           two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 1)),
-                           two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 2)),
-                           two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 3))));
+      at_f16x8, make_uint4(two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0)),
+                           two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1)),
+                           two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2)),
+                           two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3))));
 }
 
 // the bytes of 255

@@ -4,15 +4,16 @@
 // KV head's group) of one request, 32 to a wave, and walks its tokens in tiles of 64, whose
 // codes are converted once, on their way into LDS.
 //   - Keys become bf16 with their scales, exact.
-//   - Values become fp16. In a tile that all rows see whole, a value takes its scale along,
-//     relative to the largest of the 16 tokens' (of its unit, 2^lv), and 2^lv enters with the
-//     exponential's argument and leaves the sum of weights once a unit. In one that some
-//     rows see in part (the end of each row), values stay plain codes, and the scales of the
-//     tokens that a row sees go to its probabilities, a group of 32 dims at a time, as in
-//     attend4.hpp: nothing of a row comes from tokens that it does not see, and a NaN scale
-//     reaches just the rows that see it. (Units that a wave's rows see whole or not at all
-//     share their factors there too: a prompt of 8192 tokens with a row of one token in every
-//     workgroup 1300 us without that, 752 with it, 577 without such rows.)
+//   - Values become fp16, doubled: whole numbers, exact with factors down to fp16's least,
+//     2^-24. In a tile that all rows see whole, a value takes its scale along, relative to the
+//     largest of the 16 tokens' (of its unit, 2^lv), and 2^lv enters with the exponential's
+//     argument and leaves the sum of weights once a unit. In one that some rows see in part
+//     (the end of each row), values stay plain codes, and the scales of the tokens that a row
+//     sees go to its probabilities, a group of 32 dims at a time, as in attend4.hpp: nothing
+//     of a row comes from tokens that it does not see, and a NaN scale reaches just the rows
+//     that see it. (Units that a wave's rows see whole or not at all share their factors there
+//     too: a prompt of 8192 tokens with a row of one token in every workgroup 1300 us without
+//     that, 752 with it, 577 without such rows.)
 //   - The reference of a row's sums is the running maximum of score + lv, moved when it has
 //     grown by 2^kLazy or more.
 // Two prompts of 8009 and 8192 tokens, 32 heads on 8: 1.12 ms, 0.96 PFLOP/s (a large library
@@ -223,8 +224,8 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     p[32] = __builtin_bit_cast(uint4, codes4_bf16(kreg.y, s));
   };
   auto store_v = [&](int c) {
-    uint4 x = __builtin_bit_cast(uint4, codes4_f16(vreg.x));
-    uint4 y = __builtin_bit_cast(uint4, codes4_f16(vreg.y));
+    uint4 x = __builtin_bit_cast(uint4, codes4_f16(vreg.x, 2.f));
+    uint4 y = __builtin_bit_cast(uint4, codes4_f16(vreg.y, 2.f));
     if (!in_part(c)) {
       const uint4* f =
           reinterpret_cast<const uint4*>(&lds.factor[(begin + c) % 3][vu][4 * (vd >> 5)]);
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
     p[kP4Frag] = y;
   };
 
-  // the wave's state: sums in units of 2^m
+  // the wave's state: weights in units of 2^m, sums of values in half of that
   at_f32x16 o[4];
 #pragma unroll
   for (int dt = 0; dt < 4; ++dt)
@@ -469,7 +470,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
   // lane: dims 32 dt + 8 q + 4 half + e of its row
   if (splits == 1) {
     const bool none = l == 0.f;
-    const float inv = none ? 0.f : 1.f / l;
+    const float inv = none ? 0.f : 0.5f / l;
     uint16_t* out = a.out + (tok * a.Hq + hq) * kHeadDim;
 #pragma unroll
     for (int dt = 0; dt < 4; ++dt)
@@ -487,7 +488,7 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<at_f32x4*>(out + 32 * dt + 8 * g + 4 * half) =
-            at_f32x4{o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]};
+            at_f32x4{o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]} * 0.5f;
     if (half == 0) {
       a.part_ml[2 * part] = m;
       a.part_ml[2 * part + 1] = l;

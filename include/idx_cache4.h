@@ -72,11 +72,11 @@ int idx_cache4_read(const int32_t* slots, const uint8_t* k_cache, const uint8_t*
  * of sizes and workspaces, with these differences:
  *   - a key meets its query as exact bf16 products with its scales in the key (no limit
  *     of their ratios): x is scale times their fp32 sum;
- *   - a probability is rounded to 11 bits (fp16), then takes its value's scale, relative to
- *     the largest that the row sees among its unit (16 tokens from a multiple of 16 on; one
- *     2^25 or more below that counts as zero), and meets the code, exact there; a product of
- *     weight and scale is off by up to 2^-33 of the row's largest product of a weight and its
- *     unit's largest scale;
+ *   - a probability is rounded to 11 bits (fp16); it, or its value's code, which is exact,
+ *     takes the value's scale, relative to the largest that the row sees among its unit (16
+ *     tokens from a multiple of 16 on; one 2^25 or more below that counts as zero); a product
+ *     of weight and scale is off by up to 2^-33 of the row's largest product of a weight and
+ *     its unit's largest scale;
  *   - value scales are NaN or from 2^IDX_CACHE4_MIN_EXP to 2^IDX_CACHE4_MAX_EXP, as the
  *     write gives them (others: the outputs of the rows that see them are unspecified).
  * A NaN scale makes NaN of what it reaches: of a key, the rows that see the token; of a

@@ -14,6 +14,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from oracle import cache4 as c4
 from oracle import paged_cache as pc
 from tests.cache4_helpers import Cache4
 from tests.cache_helpers import U
@@ -113,3 +114,38 @@ def test_many_least_scales_beside_one_largest(n, at, gap):
     q[0] = gap
     for name, out in forms(c, q, n, np.log(2)):
         check(f"{n} tokens, {at}, 2^{gap}: {name}", out, c, q, n, np.log(2))
+
+
+@pytest.mark.parametrize("code", [1, 3, 7, 9])
+@pytest.mark.parametrize("below", [20, 22, 23, 24])
+def test_blocks_far_below_their_units_largest_scale(below, code):
+    """A block of dims whose scales lie 2^below under those of another block of the same
+    tokens, codes of one sign."""
+    n = 400
+    c = plain_cache(n)
+    c.v[:, :, 64:96] = code
+    c.vs[:, :, 2] = 127 - below
+    c.poison_tails()
+    q = torch.zeros(128)
+    for name, out in forms(c, q, n, 1.0):
+        check(f"2^-{below} of code {code}: {name}", out, c, q, n, 1.0)
+        want = c4.e2m1_values()[code] * 2.0 ** -below
+        assert float((out[..., 64:96].double() / want - 1).abs().max()) < 2.0 ** -6
+
+
+@pytest.mark.parametrize("below", [10, 17, 24])
+def test_tokens_far_below_their_units_largest_scale(below):
+    """All tokens of a unit but one have scales 2^below under it, and the weight."""
+    n = 400
+    c = plain_cache(n)
+    key = np.zeros(128, np.uint8)
+    key[0] = 2
+    for t in range(n):
+        if t % 16 != 5:
+            put(c, t, "k", key, 127)
+            put(c, t, "v", 3, 127 - below)
+    c.poison_tails()
+    q = torch.zeros(128)
+    q[0] = float(below)
+    for name, out in forms(c, q, n, np.log(2)):
+        check(f"2^-{below}: {name}", out, c, q, n, np.log(2))
