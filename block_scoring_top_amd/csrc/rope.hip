@@ -136,14 +136,23 @@ __global__ __launch_bounds__(kRopeNT) void rope_kernel(RopeArgs a, bool copy_q, 
         store8<BF16>(dst, to + d + pairs, w);
       }
     } else if (is_q ? copy_q : copy_k) {
-      // the dims beside the rotated part, in two runs of 8
+      // the dims beside the rotated part, in two runs of 8, as they are
       int d = 16 * j - a.rot, e = d + 8;
       d += d < a.first ? 0 : a.rot;
       e += e < a.first ? 0 : a.rot;
-      load8<BF16>(src, from + d, x);
-      load8<BF16>(src, from + e, y);
-      store8<BF16>(dst, to + d, x);
-      store8<BF16>(dst, to + e, y);
+      if constexpr (BF16) {  // (a conversion to float and back would quieten NaN)
+        const uint16_t* p = static_cast<const uint16_t*>(src) + from;
+        uint16_t* q = static_cast<uint16_t*>(dst) + to;
+        const uint4 u = *reinterpret_cast<const uint4*>(p + d);
+        const uint4 w = *reinterpret_cast<const uint4*>(p + e);
+        *reinterpret_cast<uint4*>(q + d) = u;
+        *reinterpret_cast<uint4*>(q + e) = w;
+      } else {
+        load8<BF16>(src, from + d, x);
+        load8<BF16>(src, from + e, y);
+        store8<BF16>(dst, to + d, x);
+        store8<BF16>(dst, to + e, y);
+      }
     }
   }
 }
