@@ -78,7 +78,7 @@ struct Cache8 {
 // more than 2^-29 of a row's weights, 2^-57 at the least (1024 items of 64 splits: 0.9 us if it
 // always did).
 constexpr float kHeavy = 0x1p40f;
-template <int TEAMS>
+template <int TEAMS, bool ALL>
 __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t items,
                                                              int splits) {
   constexpr int kItems = kAtNT / 32 / TEAMS;  // of a workgroup
@@ -97,10 +97,11 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
   at_f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
     // A split without tokens has no weight: its sums are not taken, whatever they hold. Few
-    // items ask for two steps' weights and sums at once, many save those splits' bytes (1024
-    // items of 64 splits, 40 of them empty: 7.5 us, 8.5 with all sums read).
-    constexpr int kStep = 4, kLoads = TEAMS == 8 ? 2 : 1;
-    const bool all = TEAMS == 8 && items * splits <= 8192;
+    // items (ALL) ask for two steps' weights and sums at once, many save those splits' bytes
+    // (1024 items of 64 splits, 40 of them empty: 7.5 us, 8.5 with all sums read) and the
+    // registers of the second step (51 against 82, eight waves a SIMD against five: 32 rows of
+    // 8192 to 32768 tokens, 64 heads on 4, 152 us in all with it, 150 without).
+    constexpr int kStep = 4, kLoads = ALL ? 2 : 1;
     for (int s0 = team; s0 < splits; s0 += kLoads * kStep * TEAMS) {
       at_f32x2 ml[kLoads * kStep];
       at_f32x4 x[kLoads * kStep];
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
       for (int i = 0; i < kLoads * kStep; ++i) {
         const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
         ml[i] = *reinterpret_cast<const at_f32x2*>(a.part_ml + 2 * p);
-        if (all)
+        if constexpr (ALL)
           x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
         if (s0 + i * TEAMS >= splits) ml[i] = at_f32x2{-__builtin_inff(), 0.f};
       }
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(kAtNT) void attend_merge_kernel(AttnArgs a, int64_t
       for (int i = 0; i < kLoads * kStep; ++i) {
         if (ml[i][1] == 0.f) {
           x[i] = at_f32x4{0.f, 0.f, 0.f, 0.f};
-        } else if (!all) {
+        } else if (!ALL) {
           const int64_t p = first + (int64_t)min(s0 + i * TEAMS, splits - 1) * G;
           x[i] = *reinterpret_cast<const at_f32x4*>(a.part_o + p * kHeadDim + 4 * lane);
         }
@@ -203,10 +204,12 @@ int launch_attend_merge(const AttnArgs& a, int splits, void* stream) {
   const bool wide = splits > 8 && items <= 8192;
   const int per = wide ? 1 : 4;
   const dim3 grid((unsigned)((items + per - 1) / per)), blk(kAtNT);
-  if (wide)
-    hipLaunchKernelGGL((attend_merge_kernel<8>), grid, blk, 0, s, a, items, splits);
+  if (wide && items * splits <= 8192)
+    hipLaunchKernelGGL((attend_merge_kernel<8, true>), grid, blk, 0, s, a, items, splits);
+  else if (wide)
+    hipLaunchKernelGGL((attend_merge_kernel<8, false>), grid, blk, 0, s, a, items, splits);
   else
-    hipLaunchKernelGGL((attend_merge_kernel<2>), grid, blk, 0, s, a, items, splits);
+    hipLaunchKernelGGL((attend_merge_kernel<2, false>), grid, blk, 0, s, a, items, splits);
   return (int)hipGetLastError();
 }
 
