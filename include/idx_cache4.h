@@ -71,7 +71,9 @@ int idx_cache4_read(const int32_t* slots, const uint8_t* k_cache, const uint8_t*
  * the 4-bit cache: the same rows, lists, selections, masks, caps, biases, outputs, limits
  * of sizes and workspaces, with these differences:
  *   - a key meets its query as exact bf16 products with its scales in the key (no limit
- *     of their ratios): x is scale times their fp32 sum;
+ *     of their ratios): x is scale times their fp32 sum. Key scales are NaN or from 2^-125
+ *     to 2^125, and |q| times the largest that a row sees is at most 2^117 (in place of
+ *     idx_cache.h's limit of |q|; a sum reaches 768 times that);
  *   - a probability is rounded to 11 bits (fp16); it, or its value's code, which is exact,
  *     takes the value's scale, relative to the largest that the row sees among its unit (16
  *     tokens from a multiple of 16 on; one 2^25 or more below that counts as zero); a product

@@ -149,3 +149,23 @@ def test_tokens_far_below_their_units_largest_scale(below):
     q[0] = float(below)
     for name, out in forms(c, q, n, np.log(2)):
         check(f"2^-{below}: {name}", out, c, q, n, np.log(2))
+
+
+def test_largest_queries_and_keys():
+    """|q| times the largest key scale up to 2^117, key scales from 2^-125 to 2^125: the
+    products and their sums stay within fp32."""
+    n = 150
+    rng = np.random.default_rng(6)
+    for exp, low, high in ((57, 0, 60), (117, -125, 0), (-8, 100, 125), (117, 0, 0)):
+        c = plain_cache(n)
+        c.k[:] = rng.integers(0, 16, c.k.shape)
+        c.k[c.pages(0)[1]] = 7                 # keys of 6 everywhere, in the largest scale
+        c.ks[:] = 127 + rng.integers(low, high + 1, c.ks.shape)
+        c.ks[c.pages(0)[1]] = 127 + high
+        c.v[:] = rng.integers(0, 16, c.v.shape)
+        c.poison_tails()
+        for sign in (np.ones(128), rng.choice([-1.0, 1.0], 128)):
+            q = torch.from_numpy(sign * 2.0 ** exp).float()
+            scale = 2.0 ** -(exp + high) / 256
+            for name, out in forms(c, q, n, scale):
+                check(f"q 2^{exp}, keys 2^{low}..2^{high}: {name}", out, c, q, n, scale)
