@@ -169,3 +169,77 @@ def test_largest_queries_and_keys():
             scale = 2.0 ** -(exp + high) / 256
             for name, out in forms(c, q, n, scale):
                 check(f"q 2^{exp}, keys 2^{low}..2^{high}: {name}", out, c, q, n, scale)
+
+
+def far_apart(seed, n):
+    """Scales 2^0 to 2^-24 of their unit's largest, a block 2^-20 or less of it; its codes are of
+    one sign, so that its outputs are as large as they can be."""
+    c = Cache4(seed, [n], 2, 16)
+    c.vs[:] = 127 - c.rng.integers(0, 25, c.vs.shape)
+    c.vs[:, :, 2] = 127 - c.rng.integers(20, 25, c.vs[:, :, 2].shape)
+    c.vs[:, :, 0, 0] = 127
+    c.v[:, :, 64:96] &= 7
+    c.v[:, :, 64:96] |= 1
+    c.poison_tails()
+    return c
+
+
+def rows_within(name, c, q, out, seen):
+    """Rows out [n, Hq, 128] of request 0, each with its own query and length. The bound sees
+    the small block: zeros in its place would be outside."""
+    out, q = out.double().cpu().numpy(), q.double().numpy()
+    worst, blind, count = 0.0, 0, 0
+    for r in range(len(out)):
+        for hq in range(out.shape[1]):
+            want, tol = expected(c, q[r, hq], 0, int(seen[r]), float(np.float32(128 ** -0.5)),
+                                 hq * 2 // out.shape[1])
+            err = np.abs(out[r, hq] - want) / tol
+            assert (err <= 1).all(), (name, r, hq, int(err.argmax()), float(err.max()))
+            worst = max(worst, float(err.max()))
+            blind += int((np.abs(want[64:96]) <= tol[64:96]).sum())
+            count += 32
+    print(f"[range4] {name}: {worst:.2f} of the bound, {blind} of {count} unseen", flush=True)
+    assert blind < count / 50
+
+
+@pytest.mark.parametrize("Hq", [2, 8, 40])
+@pytest.mark.parametrize("n", [16, 47, 64, 90])
+def test_scales_far_apart_single_rows(n, Hq):
+    c = far_apart(n, n)
+    q = torch.from_numpy(c.rng.standard_normal((4, Hq, 128))).bfloat16()
+    seen = np.array([n, n, max(1, n - 9), n - n % 16])
+    out = idx.idx_attend4(q.cuda(), *c.device(), i32(seen), c.max_pages, row_req=i32([0] * 4))
+    rows_within(f"{n} tokens, {Hq} heads", c, q, out, seen)
+
+
+@pytest.mark.parametrize("shape", ["few", "whole", "mixed", "causal"])
+def test_scales_far_apart_packed_rows(shape):
+    """Few packed rows; a prompt whose rows see all of it, whose workgroups hold shorter rows
+    too, or whose rows each see one token more."""
+    n = 128
+    t = 5 if shape == "few" else 110
+    c = far_apart(t, n)
+    q = torch.from_numpy(c.rng.standard_normal((t, 4, 128))).bfloat16()
+    seen = np.full(t, n)
+    if shape == "mixed":
+        seen[::3] = c.rng.integers(1, n, len(seen[::3]))
+    if shape in ("causal", "few"):
+        seen = np.arange(n - t, n) + 1
+    out = idx.idx_attend4_prefill(q.cuda(), *c.device(), i32([0, t]), i32(seen), c.max_pages)
+    step = slice(None, None, 1 + t // 30)
+    rows_within(shape, c, q[step], out[step], seen[step])
+
+
+def test_other_rows_lengths_leave_a_row_within_its_bound():
+    """A prompt's row that keeps its own length while the others' change: the kernel may take
+    another way through its tiles; both results are within the bound."""
+    n, t = 128, 120
+    c = far_apart(3, n)
+    q = torch.from_numpy(c.rng.standard_normal((t, 4, 128))).bfloat16()
+    keep = np.arange(0, t, 4)
+    for other in (n, n - 1, 70, 1, 0):
+        seen = np.full(t, other)
+        seen[keep] = n
+        out = idx.idx_attend4_prefill(q.cuda(), *c.device(), i32([0, t]), i32(seen), c.max_pages)
+        rows_within(f"others see {other}", c, q[keep], out[torch.from_numpy(keep).cuda()],
+                    seen[keep])
