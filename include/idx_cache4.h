@@ -83,7 +83,8 @@ int idx_cache4_read(const int32_t* slots, const uint8_t* k_cache, const uint8_t*
  *     write gives them (others: the outputs of the rows that see them are unspecified).
  * A NaN scale makes NaN of what it reaches: of a key, the rows that see the token; of a
  * value, its 32 dims of those rows. Bytes of tokens that a row does not see do not reach it,
- * whatever they are.
+ * whatever they are. The visible lengths of other rows of a prompt decide whether weight or
+ * code takes the scale: a row's bits may differ with them, within the bounds above.
  */
 size_t idx_attend4_workspace_bytes(int R, int Hq, int Hkv, int max_pages, int K, int page_size);
 int idx_attend4(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
