@@ -821,8 +821,9 @@ def idx_rope(q, k, tok_len, turns, first=0, interleaved=False, inverse=False, fa
     token's position tok_len - 1 (PageTables.tok_len; a row of 0 keeps its outputs), rot =
     2 * len(turns), the table of idx_rope_table or idx_rope_turns. Pairs are halves of the
     part, or neighbours with `interleaved`; `inverse` turns back (with the same factor: the
-    gradient). Into new tensors, or q_out and k_out, which may be q and k themselves.
-    Returns (q_out, k_out)."""
+    gradient, which autograd does not take by itself). Into new tensors, or q_out and k_out,
+    which may be q and k themselves; rows without a token hold anything in new ones. Returns
+    (q_out, k_out)."""
     lib = _lib or load()
     dev = _gpu(q)
     qs = _rows("q", q, dev)

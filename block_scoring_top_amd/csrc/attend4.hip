@@ -20,8 +20,12 @@ namespace idxk {
 // two a CU, all that it holds, where a chunk is more than its start and its part of the join:
 // groups above 16 heads, whose instance has two workgroups a CU and twice the partial sums
 // (16 rows of 8192 to 32768 tokens, 64 heads on 2: 51 us with eight, 40 with two; 4 of 4096 to
-// 131072: 45 and 37), and a row by itself (131072 tokens, 32 heads on 8: 42 and 35). Ragged rows
-// of smaller groups: 4 of 4096 to 131072, 32 heads on 8, 70 with eight, 82 with two.
+// 131072: 45 and 37), and a row by itself (131072 tokens, 32 heads on 8: 41 and 36). Several rows
+// of smaller groups are ragged as a rule (4096 to 131072, 32 heads on 8: two 42 us with eight, 46
+// with two; four 70 and 82; 16 259 and 293); equal ones lose a little by it (two of 131072 64
+// and 59, four 114 and 109). From 512 rows times heads on rows stay whole, two workgroups a CU
+// or more (64 rows of 8192 tokens, 8 heads: 105 us whole, 115 in two; of 2048 to 32768: 277
+// and 309).
 AttnSplit attend4_rows_split(int64_t R, int Hkv, int G, int64_t units) {
   const int64_t tiles = (units + 3) / 4, pairs = R * Hkv;
   const int64_t want = G > 16 || R == 1 ? 512 : 2048;

@@ -16,8 +16,8 @@
 //     that, 752 with it, 577 without such rows.)
 //   - The reference of a row's sums is the running maximum of score + lv, moved when it has
 //     grown by 2^kLazy or more.
-// Two prompts of 8009 and 8192 tokens, 32 heads on 8: 1.12 ms, 0.96 PFLOP/s (a large library
-// product reaches 1.21 on this card). Bound by the products and the exponentials beside them
+// Two prompts of 8009 and 8192 tokens, 32 heads on 8: 1.12 to 1.20 ms by card, up to 0.96
+// PFLOP/s (a large library product reaches 1.21). Bound by the products and the exponentials beside them
 // at the clock that the card holds under both. What led there: 2.93 ms with 16 rows a product
 // straight from the cache; 1.24 as described; 1.21 with the scales' factors made by one wave
 // a tile instead of each thread's own; 1.17 with the tokens' largest scales found once and
@@ -498,7 +498,11 @@ __global__ __launch_bounds__(kP4NT) void attend4_prefill_kernel(AttnArgs a, int 
 
 }  // namespace
 
-// How packed calls are cut: as the 8-bit cache's.
+// How packed calls are cut: as the 8-bit cache's. The switch between the kernels, 64 rows a
+// request, is early for this cache, whose 16-row kernel converts half the bytes: 9 requests of
+// 5104 to 62488 tokens, 8 heads, 64 rows each 207 us there and 428 here, 96 rows 291 and 573,
+// 128 rows 434 and 367; 64 requests of 2000 to 8000, 64 rows 199 and 440, 128 rows 347 and 437,
+// 256 rows 639 and 822.
 AttnSplit attend4_prefill_split(int64_t n_tok, int B, int Hq, int Hkv, int64_t units) {
   return attend_prefill_split(n_tok, B, Hq, Hkv, units);
 }
