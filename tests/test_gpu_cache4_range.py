@@ -31,16 +31,20 @@ def i32(a):
     return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
 
 
-def expected(c, q, b, seen, scale, h=0):
+def expected(c, q, b, seen, scale, h=0, cap=0.0, slope=0.0):
     """One row and query head q [128]: its output and how far off it may be."""
     k, v, there, top = c.tokens(b, h)
-    out, absum, mag = pc.attend(q, k, v, there, seen, None, c.page, scale)
+    out, absum, mag = pc.attend(q, k, v, there, seen, None, c.page, scale, cap, slope)
     n = min(seen, len(k))
     x = k[:n] @ q * scale
+    if cap:
+        x = cap * np.tanh(x / cap)
+    x -= slope * (seen - 1 - np.arange(n))
     w = np.exp(x - x.max())
     w /= w.sum()
     unit = np.pad(top[:n], (0, -n % 16)).reshape(-1, 16).max(1).repeat(16)[:n]
-    weights = 2 * np.expm1(160 * U * mag + 4 * U) + 2.0 ** -11 + (2 * n + 8) * U
+    e = 160 * U * mag + 16 * U * (cap + slope * n) + 4 * U
+    weights = 2 * np.expm1(e) + 2.0 ** -11 + (2 * n + 8) * U
     off = absum * weights + n * 6 * 2.0 ** -33 * float((w * unit).max())
     return out, off + (np.abs(out) + off) * 2.0 ** -8 + 2.0 ** -130
 
@@ -243,3 +247,29 @@ def test_other_rows_lengths_leave_a_row_within_its_bound():
         out = idx.idx_attend4_prefill(q.cuda(), *c.device(), i32([0, t]), i32(seen), c.max_pages)
         rows_within(f"others see {other}", c, q[keep], out[torch.from_numpy(keep).cuda()],
                     seen[keep])
+
+
+@pytest.mark.parametrize("cap,biased", [(0.0, False), (60.0, False), (300.0, False), (0.0, True)])
+@pytest.mark.parametrize("n,t,Hq", [(90, 4, 8), (700, 6, 40), (700, 140, 4), (3000, 130, 8)])
+def test_pages_of_any_scales(n, t, Hq, cap, biased):
+    """Each page with value scales of its own anywhere in the range, and scores far apart: rows
+    one by one, and packed, each seeing a token more than the one before."""
+    c = Cache4(n + t, [n], 2, 16)
+    c.vs[:] = 127 + c.rng.integers(-57, 58, (c.n_pages, 2, 1, 1)) + c.rng.integers(-3, 4, c.vs.shape)
+    c.poison_tails()
+    q = torch.from_numpy(c.rng.standard_normal((t, Hq, 128)) * 8).bfloat16()
+    slopes = np.exp2(-8 * np.arange(1, Hq + 1) / Hq).astype(np.float32) if biased else None
+    kw = dict(softcap=cap, slopes=None if slopes is None else torch.from_numpy(slopes).cuda())
+    seen = np.arange(n - t, n) + 1
+    args = (q.cuda(), *c.device())
+    outs = {"rows": idx.idx_attend4(*args, i32(seen), c.max_pages, row_req=i32([0] * t), **kw),
+            "packed": idx.idx_attend4_prefill(*args, i32([0, t]), i32(seen), c.max_pages, **kw)}
+    for name, out in outs.items():
+        out = out.double().cpu().numpy()
+        for r in sorted({0, 1, t // 2, t - 1}):
+            for hq in range(0, Hq, 1 + Hq // 8):
+                want, tol = expected(c, q[r, hq].double().numpy(), 0, int(seen[r]),
+                                     float(np.float32(128 ** -0.5)), hq * 2 // Hq, cap,
+                                     0.0 if slopes is None else float(slopes[hq]))
+                err = np.abs(out[r, hq] - want) / tol
+                assert (err <= 1).all(), (name, r, hq, int(err.argmax()), float(err.max()))
